@@ -367,6 +367,108 @@ w4a8_status_t w8a8_gemm(const int8_t* X, const float* sx, const int8_t* wq8,
                         int K, int splitk, void* workspace,
                         size_t workspace_bytes, hipStream_t stream);
 
+/*
+ * Layers whose rows choose their own weights: a router picks the experts of
+ * every token (w4a8_route), a few tokens pass through a whole
+ * mixture-of-experts layer (w4a8_moe), and the rows of a shared projection
+ * each add the low-rank adapter of their request (w4a8_gemm_lora).  The
+ * conventions above hold; outputs and workspace overlap no other argument,
+ * and calls that share a workspace must be ordered on one stream.  A call
+ * whose arguments are device arrays of choices (ids, adapter) reads them on
+ * the device, so a captured graph follows their contents.
+ */
+#define W4A8_MAX_EXPERTS 512
+#define W4A8_MAX_TOPK 16
+#define W4A8_MOE_MAX_TOKENS 256
+#define W4A8_LORA_MAX_RANK 128
+
+/*
+ * Top-k gating of router logits and the grouping of the chosen slots.
+ *   logits: [T][E] elements of in_type (W4A8_IN_*), 16-byte aligned, widened
+ *     to float32 (exact).  An expert whose logit is -inf or NaN is not
+ *     available to that token.
+ *   ids[t][j]     int32 [T][k]: the expert with the j-th largest logit (ties
+ *     go to the lowest index), -1 where fewer than j+1 are available;
+ *   weights[t][j] float32 [T][k]: e_j / sum of e over the token's available
+ *     experts (renormalize 0) or over its chosen ones (renormalize 1), with
+ *     e_i = exp(x_i - max x), 1 where x_i equals the maximum (so +inf logits
+ *     share the weight); 0 where ids is -1;
+ *   offsets       int32 [E+1]: experts' ranges of `rows`, as
+ *     w4a8_gemm_grouped takes them; offsets[E] = slots with an expert;
+ *   rows          int32 [T*k]: the slots t*k + j in order of expert, then
+ *     slot (row p of a grouped problem is token rows[p] / k); -1 from
+ *     offsets[E] on.
+ * 1 <= E <= W4A8_MAX_EXPERTS, 1 <= k <= min(E, W4A8_MAX_TOPK), T * E < 2^31.
+ * T = 0 writes offsets (zeros) only; the other pointers may be NULL then.
+ * ids, weights, offsets, rows: 4-byte aligned.  workspace: at least
+ * w4a8_route_workspace_size bytes (0 for a decode batch: NULL allowed),
+ * 16-byte aligned.  No atomics order anything: results are reproducible.
+ */
+size_t w4a8_route_workspace_size(int T, int E, int k);
+w4a8_status_t w4a8_route(const void* logits, int in_type, int T, int E, int k,
+                         int renormalize, int32_t* ids, float* weights,
+                         int32_t* offsets, int32_t* rows, void* workspace,
+                         size_t workspace_bytes, hipStream_t stream);
+
+/*
+ * A whole mixture-of-experts layer for at most W4A8_MOE_MAX_TOKENS tokens
+ * (longer batches: w4a8_gemm_grouped on w4a8_route's grouping).
+ *   X: [T][H] elements of in_type; ids int32 [T][k], weights float32 [T][k]
+ *     (w4a8_route's, or any: an id outside [0, E) is no expert, a token may
+ *     name an expert twice);
+ *   wq13, s13, a13, sw13: the experts' w4a8_pack outputs (LQQ) of
+ *     W13[e] = float32 [2F][H], gate rows 0..F-1, up rows F..2F-1, laid end
+ *     to end as for w4a8_gemm_grouped; wq2, s2, a2, sw2: those of
+ *     W2[e] = [H][F]; one group size for both.
+ * Per slot (t, j) with expert e, all in float32 unless said:
+ *   Xq, sx = INT8 of token t as w4a8_quant_act;
+ *   g, u = ((exact int32 product) * sx) * sw13[e], h = g / (1 + exp(-g)) * u;
+ *   hq, sh = INT8 of h as w4a8_quant_act; y = ((int32 product) * sh) * sw2[e];
+ *   Y[t] = sum over j (ascending) of weights[t][j] * y, rounded once to
+ *   out_type (W4A8_IN_*).  A slot of weight 0 adds nothing, a token without
+ *   an expert gives zeros.  A token with an element that is not finite, or
+ *   whose h overflows float32, gives NaN (other tokens are unaffected).
+ * H % 128 = 0, F % 128 = 0, both < 2^19, 2 F H < 2^32; 1 <= E <=
+ * W4A8_MAX_EXPERTS, 1 <= k <= W4A8_MAX_TOPK.  X, Y and the byte arrays
+ * 16-byte aligned, the others 4-byte.  workspace: w4a8_moe_workspace_size
+ * bytes, 16-byte aligned, contents ignored and undefined afterwards.
+ */
+size_t w4a8_moe_workspace_size(int T, int E, int k, int H, int F);
+w4a8_status_t w4a8_moe(const void* X, int in_type, const int32_t* ids,
+                       const float* weights, int T, int E, int k,
+                       const uint8_t* wq13, const uint8_t* s13,
+                       const uint8_t* a13, const float* sw13,
+                       const uint8_t* wq2, const uint8_t* s2,
+                       const uint8_t* a2, const float* sw2, void* Y,
+                       int out_type, int H, int F, int group, void* workspace,
+                       size_t workspace_bytes, hipStream_t stream);
+
+/*
+ * A shared W4A8 projection with the low-rank adapter each row selects:
+ *   Y[m] = fp16_rne( (acc[m] * sx[m]) * sw
+ *                    + scale[a] * (X[m] . A[a]^T) . B[a]^T ),  a = adapter[m]
+ * acc as w4a8_gemm on the INT8 rows (Xq, sx) that w4a8_quant_act_ex gives
+ * for X; the adapter's products are float32 sums over the stored values (the
+ * inner one is kept to at least 16 significant bits), and Y is rounded once.
+ *   X: [M][K], A: [n_adapters][R][K], B: [n_adapters][N][R], all fp16 or all
+ *     bfloat16 (in_type); scale: float32 [n_adapters]; adapter: int32 [M],
+ *     values outside [0, n_adapters) select none, in any order.  Adapters of
+ *     smaller rank are padded with zero rows of A (or columns of B).
+ *   wq, s_u8, a_u8, sw: w4a8_pack (LQQ) of the shared weights.
+ * R a multiple of 8, 8 <= R <= W4A8_LORA_MAX_RANK; n_adapters = 0 is
+ * w4a8_gemm (A, B, scale unread).  Sizes as w4a8_gemm.  X, A, B, Y and the
+ * byte arrays 16-byte aligned, the others 4-byte.  workspace:
+ * w4a8_gemm_lora_workspace_size bytes, 16-byte aligned.
+ */
+size_t w4a8_gemm_lora_workspace_size(int M, int N, int K, int R);
+w4a8_status_t w4a8_gemm_lora(const void* X, int in_type, const uint8_t* wq,
+                             const uint8_t* s_u8, const uint8_t* a_u8,
+                             const float* sw, const void* A, const void* B,
+                             const float* scale, int n_adapters, int R,
+                             const int32_t* adapter, void* Y, int M, int N,
+                             int K, int group, void* workspace,
+                             size_t workspace_bytes, hipStream_t stream);
+
 /* Static English text for a status code (never NULL). */
 const char* w4a8_status_str(w4a8_status_t status);
 

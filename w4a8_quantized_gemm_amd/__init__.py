@@ -39,12 +39,15 @@ OUT_BF16, OUT_F32 = 0, 1
 IN_F32, IN_F16, IN_BF16 = 0, 1, 2
 ABL_LQQ, ABL_AFFINE16, ABL_LQQ_COARSE = 0, 1, 2
 LAYOUT_VERSION = 1
+MAX_EXPERTS, MAX_TOPK, MOE_MAX_TOKENS, LORA_MAX_RANK = 512, 16, 256, 128
 
 EXPORTS = ("w4a8_pack", "w4a8_quant_act", "w4fp8_quant_act",
            "w4a8_quant_act_ex", "w4fp8_quant_act_ex", "w4a8_workspace_size", "w4a8_gemm",
            "w4a8_gemm_noalloc", "w4a8_gemm_plan",
            "w4a8_gemm_ablation", "w4a8_gemm_grouped", "w4fp8_gemm", "w4fp8g_pack",
            "w4fp8g_gemm", "w8a8_pack", "w8a8_gemm",
+           "w4a8_route_workspace_size", "w4a8_route", "w4a8_moe_workspace_size", "w4a8_moe",
+           "w4a8_gemm_lora_workspace_size", "w4a8_gemm_lora",
            "w4a8_status_str", "w4a8_last_hip_error", "w4a8_layout_version")
 
 _P, _I, _Z = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t
@@ -65,6 +68,17 @@ lib.w4fp8g_pack.argtypes = [_P, _I, _I, _I, _P, _P, _P, _P]
 lib.w4fp8g_gemm.argtypes = [_P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _P, _Z, _P]
 lib.w8a8_pack.argtypes = [_P, _I, _I, _P, _P, _P]
 lib.w8a8_gemm.argtypes = [_P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _P, _Z, _P]
+lib.w4a8_route_workspace_size.argtypes = [_I, _I, _I]
+lib.w4a8_route_workspace_size.restype = _Z
+lib.w4a8_route.argtypes = [_P, _I, _I, _I, _I, _I, _P, _P, _P, _P, _P, _Z, _P]
+lib.w4a8_moe_workspace_size.argtypes = [_I, _I, _I, _I, _I]
+lib.w4a8_moe_workspace_size.restype = _Z
+lib.w4a8_moe.argtypes = [_P, _I, _P, _P, _I, _I, _I, _P, _P, _P, _P, _P, _P, _P, _P, _P, _I, _I,
+                         _I, _I, _P, _Z, _P]
+lib.w4a8_gemm_lora_workspace_size.argtypes = [_I, _I, _I, _I]
+lib.w4a8_gemm_lora_workspace_size.restype = _Z
+lib.w4a8_gemm_lora.argtypes = [_P, _I, _P, _P, _P, _P, _P, _P, _P, _I, _I, _P, _P, _I, _I, _I,
+                               _I, _P, _Z, _P]
 lib.w4a8_status_str.argtypes = [_I]
 lib.w4a8_status_str.restype = ctypes.c_char_p
 lib.w4a8_last_hip_error.restype = _I
@@ -72,7 +86,7 @@ lib.w4a8_layout_version.restype = _I
 for _n in ("w4a8_pack", "w4a8_quant_act", "w4fp8_quant_act", "w4a8_quant_act_ex",
            "w4fp8_quant_act_ex", "w4a8_gemm", "w4a8_gemm_noalloc", "w4a8_gemm_ablation", "w4a8_gemm_grouped",
            "w4fp8_gemm", "w4fp8g_pack", "w4fp8g_gemm", "w8a8_pack", "w8a8_gemm",
-           "w4a8_gemm_plan"):
+           "w4a8_gemm_plan", "w4a8_route", "w4a8_moe", "w4a8_gemm_lora"):
     getattr(lib, _n).restype = _I
 
 assert lib.w4a8_layout_version() == LAYOUT_VERSION
@@ -442,3 +456,213 @@ def gemm_w8a8(Xq, sx, packed, out_type: int = OUT_F16, splitk: int = 0, out=None
                          out_type, M, N, K, splitk, _ptr(workspace), ws_bytes, _stream(stream)),
            "w8a8_gemm")
     return Y
+
+
+# ------------------------------- layers whose rows choose their own weights ----
+#
+# These run on the device of their first tensor, whatever the current device
+# is; every tensor must live there.  Outputs and workspaces that are not given
+# are allocated on the stream the call runs on.
+
+def _ready(t, dtype, shape, device, name):
+    """A contiguous tensor of this type and shape on this device."""
+    torch = _torch()
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.device != device:
+        raise ValueError(f"{name} must be on {device}, got {t.device}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+
+
+def _float_type(t, name, types=("float32", "float16", "bfloat16")):
+    torch = _torch()
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    codes = {"float32": IN_F32, "float16": IN_F16, "bfloat16": IN_BF16}
+    for n in types:
+        if t.dtype == getattr(torch, n):
+            return codes[n]
+    raise TypeError(f"{name} must be one of {', '.join(types)}, got {t.dtype}")
+
+
+def _on_gpu(t, name):
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be on a GPU device")
+    if t.dim() != 2:
+        raise ValueError(f"{name} must be a 2-D tensor")
+
+
+class _Launch:
+    """The device and stream of one call; tensors allocated inside belong to
+    that stream."""
+
+    def __init__(self, device, stream):
+        torch = _torch()
+        if stream is not None and stream.device != device:
+            raise ValueError(f"stream is on {stream.device}, the tensors on {device}")
+        self._ctx = None
+        if stream is not None:
+            self._ctx = torch.cuda.stream(stream)
+        elif torch.cuda.current_device() != device.index:
+            self._ctx = torch.cuda.device(device)
+        self._device, self._stream = device, stream
+
+    def __enter__(self):
+        if self._ctx is not None:
+            self._ctx.__enter__()
+        s = self._stream or _torch().cuda.current_stream(self._device)
+        return ctypes.c_void_p(s.cuda_stream)
+
+    def __exit__(self, *exc):
+        if self._ctx is not None:
+            self._ctx.__exit__(*exc)
+
+
+def _workspace(workspace, need, device):
+    """(tensor, bytes) of the caller's workspace, or a new one."""
+    torch = _torch()
+    if workspace is None:
+        workspace = torch.empty(need, dtype=torch.uint8, device=device) if need else None
+    elif workspace.device != device:
+        raise ValueError(f"workspace must be on {device}, got {workspace.device}")
+    elif not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    return workspace, 0 if workspace is None else workspace.numel() * workspace.element_size()
+
+
+def _packed_ready(p, keys, E, device, name):
+    torch = _torch()
+    N, K, g = p["N"], p["K"], p["group"]
+    sizes = {"wq": N * K // 2, "s_u8": N * K // g, "a_u8": N * K // g, "sw": N}
+    for k in keys:
+        _ready(p[k], torch.float32 if k == "sw" else torch.uint8, (E * sizes[k],), device,
+               f"{name}[{k!r}]")
+
+
+def route_workspace_size(T: int, E: int, k: int) -> int:
+    return int(lib.w4a8_route_workspace_size(T, E, k))
+
+
+def route(logits, k: int, renormalize: bool = True, out=None, workspace=None, stream=None):
+    """w4a8_route: top-k gating of [T][E] logits (float32, float16 or
+    bfloat16) and the grouping of the chosen slots by expert.
+
+    Returns a dict with ids (int32 [T][k], -1: no expert available), weights
+    (float32 [T][k]), offsets (int32 [E+1]) and rows (int32 [T*k], the slots
+    t*k + j by expert, -1 behind the last): ids and weights are moe()'s,
+    offsets and X[rows // k] gemm_grouped()'s.  `out`: such a dict to write
+    into."""
+    torch = _torch()
+    it = _float_type(logits, "logits")
+    _on_gpu(logits, "logits")
+    T, E = logits.shape
+    dev = logits.device
+    _ready(logits, logits.dtype, (T, E), dev, "logits")
+    if not isinstance(k, int) or not 1 <= k <= min(E, MAX_TOPK):
+        raise ValueError(f"k must be an integer in [1, {min(E, MAX_TOPK)}], got {k}")
+    with _Launch(dev, stream) as st:
+        if out is None:
+            out = {"ids": torch.empty((T, k), dtype=torch.int32, device=dev),
+                   "weights": torch.empty((T, k), dtype=torch.float32, device=dev),
+                   "offsets": torch.empty(E + 1, dtype=torch.int32, device=dev),
+                   "rows": torch.empty(T * k, dtype=torch.int32, device=dev)}
+        else:
+            _ready(out["ids"], torch.int32, (T, k), dev, "out['ids']")
+            _ready(out["weights"], torch.float32, (T, k), dev, "out['weights']")
+            _ready(out["offsets"], torch.int32, (E + 1,), dev, "out['offsets']")
+            _ready(out["rows"], torch.int32, (T * k,), dev, "out['rows']")
+        ws, ws_bytes = _workspace(workspace, route_workspace_size(T, E, k), dev)
+        _check(lib.w4a8_route(_ptr(logits), it, T, E, k, int(bool(renormalize)),
+                              _ptr(out["ids"]), _ptr(out["weights"]), _ptr(out["offsets"]),
+                              _ptr(out["rows"]), _ptr(ws), ws_bytes, st), "w4a8_route")
+    return out
+
+
+def moe_workspace_size(T: int, E: int, k: int, H: int, F: int) -> int:
+    return int(lib.w4a8_moe_workspace_size(T, E, k, H, F))
+
+
+def moe(X, ids, weights, w13, w2, out=None, workspace=None, stream=None):
+    """w4a8_moe: a mixture-of-experts layer for at most MOE_MAX_TOKENS tokens.
+
+    X: [T][H] float32, float16 or bfloat16; ids int32 / weights float32 [T][k]
+    (from route, or any; an id outside [0, E) is no expert); w13 and w2 from
+    pack_experts on [E][2F][H] (gate rows, then up rows) and [E][H][F].
+    Returns Y [T][H] in X's type, or writes into `out` (any of the three)."""
+    torch = _torch()
+    it = _float_type(X, "X")
+    _on_gpu(X, "X")
+    T, H = X.shape
+    dev = X.device
+    E, g = w13["E"], w13["group"]
+    if w2["E"] != E or w2["group"] != g:
+        raise ValueError("w13 and w2 must hold the same experts and group size")
+    F = w2["K"]
+    if w13["N"] != 2 * F or w13["K"] != H or w2["N"] != H:
+        raise ValueError(f"w13 must be [2F][H] and w2 [H][F] with H = {H}; got "
+                         f"[{w13['N']}][{w13['K']}] and [{w2['N']}][{w2['K']}]")
+    _ready(X, X.dtype, (T, H), dev, "X")
+    if not isinstance(ids, torch.Tensor) or ids.dim() != 2:
+        raise ValueError("ids must be a 2-D tensor [T][k]")
+    k = ids.shape[1]
+    _ready(ids, torch.int32, (T, k), dev, "ids")
+    _ready(weights, torch.float32, (T, k), dev, "weights")
+    for p, name in ((w13, "w13"), (w2, "w2")):
+        _packed_ready(p, ("wq", "s_u8", "a_u8", "sw"), E, dev, name)
+    with _Launch(dev, stream) as st:
+        if out is None:
+            out = torch.empty((T, H), dtype=X.dtype, device=dev)
+        ot = _float_type(out, "out")
+        _ready(out, out.dtype, (T, H), dev, "out")
+        ws, ws_bytes = _workspace(workspace, moe_workspace_size(T, E, k, H, F), dev)
+        _check(lib.w4a8_moe(_ptr(X), it, _ptr(ids), _ptr(weights), T, E, k, _ptr(w13["wq"]),
+                            _ptr(w13["s_u8"]), _ptr(w13["a_u8"]), _ptr(w13["sw"]),
+                            _ptr(w2["wq"]), _ptr(w2["s_u8"]), _ptr(w2["a_u8"]), _ptr(w2["sw"]),
+                            _ptr(out), ot, H, F, g, _ptr(ws), ws_bytes, st), "w4a8_moe")
+    return out
+
+
+def gemm_lora_workspace_size(M: int, N: int, K: int, R: int) -> int:
+    return int(lib.w4a8_gemm_lora_workspace_size(M, N, K, R))
+
+
+def gemm_lora(X, packed, lora, adapter, out=None, workspace=None, stream=None):
+    """w4a8_gemm_lora: Y [M][N] float16 = the shared W4A8 projection of X
+    (`packed` from pack) plus, per row, the low-rank adapter it selects.
+
+    X: [M][K] float16 or bfloat16, not quantised; lora: dict of A [n][R][K],
+    B [n][N][R] in X's type and scale float32 [n]; adapter: int32 [M], values
+    outside [0, n) select none."""
+    torch = _torch()
+    it = _float_type(X, "X", ("float16", "bfloat16"))
+    _on_gpu(X, "X")
+    M, K = X.shape
+    dev = X.device
+    N = packed["N"]
+    if packed["K"] != K:
+        raise ValueError("K of X and of the packed weights differ")
+    A, B = lora["A"], lora["B"]
+    if A.dim() != 3 or B.dim() != 3:
+        raise ValueError("lora['A'] must be [n][R][K] and lora['B'] [n][N][R]")
+    n, R = A.shape[0], A.shape[1]
+    _ready(X, X.dtype, (M, K), dev, "X")
+    _ready(A, X.dtype, (n, R, K), dev, "lora['A']")
+    _ready(B, X.dtype, (n, N, R), dev, "lora['B']")
+    _ready(lora["scale"], torch.float32, (n,), dev, "lora['scale']")
+    _ready(adapter, torch.int32, (M,), dev, "adapter")
+    _packed_ready(packed, ("wq", "s_u8", "a_u8", "sw"), 1, dev, "packed")
+    with _Launch(dev, stream) as st:
+        if out is None:
+            out = torch.empty((M, N), dtype=torch.float16, device=dev)
+        _ready(out, torch.float16, (M, N), dev, "out")
+        ws, ws_bytes = _workspace(workspace, gemm_lora_workspace_size(M, N, K, R), dev)
+        _check(lib.w4a8_gemm_lora(_ptr(X), it, _ptr(packed["wq"]), _ptr(packed["s_u8"]),
+                                  _ptr(packed["a_u8"]), _ptr(packed["sw"]), _ptr(A), _ptr(B),
+                                  _ptr(lora["scale"]), n, R, _ptr(adapter), _ptr(out), M, N, K,
+                                  packed["group"], _ptr(ws), ws_bytes, st), "w4a8_gemm_lora")
+    return out

@@ -136,6 +136,27 @@ bool valid_splitk(int splitk, int K) {
     return splitk <= k_tiles(K);
 }
 
+bool valid_in_type(int t) {
+    return t == W4A8_IN_F32 || t == W4A8_IN_F16 || t == W4A8_IN_BF16;
+}
+
+// Experts and choices of a router; every index of a logit or slot fits 31 bits.
+bool valid_route(int T, int E, int k) {
+    return T >= 0 && E >= 1 && E <= W4A8_MAX_EXPERTS && k >= 1 && k <= W4A8_MAX_TOPK && k <= E &&
+           (long long)T * E < (1LL << 31);
+}
+
+// The layer for a few tokens: rows of W13 [2F][H] and W2 [H][F] per expert
+// within a GEMM's limits (k <= E is the router's concern: a caller may give
+// any ids).
+bool valid_moe(int T, int E, int k, int H, int F) {
+    return T >= 0 && T <= W4A8_MOE_MAX_TOKENS && E >= 1 && E <= W4A8_MAX_EXPERTS && k >= 1 &&
+           k <= W4A8_MAX_TOPK && H > 0 && H % 128 == 0 && F > 0 && F % 128 == 0 &&
+           H < (1 << 19) && F < (1 << 19) && 2LL * F * H < (1LL << 32);
+}
+
+bool valid_rank(int R) { return R >= 8 && R <= W4A8_LORA_MAX_RANK && R % 8 == 0; }
+
 }  // namespace
 
 W4A8_EXPORT const char* w4a8_status_str(w4a8_status_t s) {
@@ -476,4 +497,133 @@ W4A8_EXPORT w4a8_status_t w8a8_gemm(const int8_t* X, const float* sx, const int8
                                                  stream));
     return hip_status(w4a8::launch_w8a8_stream(X, sx, wq8, sw, Y, out_type, M, N, K,
                                                choose_stream(M, N, K, splitk), stream));
+}
+
+W4A8_EXPORT size_t w4a8_route_workspace_size(int T, int E, int k) {
+    if (!valid_route(T, E, k) || T == 0) return 0;
+    return w4a8::plan_route(T, E, k).workspace;
+}
+
+W4A8_EXPORT w4a8_status_t w4a8_route(const void* logits, int in_type, int T, int E, int k,
+                                     int renormalize, int32_t* ids, float* weights,
+                                     int32_t* offsets, int32_t* rows, void* workspace,
+                                     size_t workspace_bytes, hipStream_t stream) {
+    if (!valid_in_type(in_type) || (renormalize != 0 && renormalize != 1))
+        return W4A8_ERR_UNSUPPORTED;
+    if (!valid_route(T, E, k)) return W4A8_ERR_SHAPE;
+    if (!offsets || (T > 0 && (!logits || !ids || !weights || !rows))) return W4A8_ERR_NULL_PTR;
+    if (!aligned4(offsets) || !aligned4(ids) || !aligned4(weights) || !aligned4(rows) ||
+        !aligned16(logits))
+        return W4A8_ERR_ALIGNMENT;
+    const size_t need = w4a8_route_workspace_size(T, E, k);
+    if (workspace_bytes < need) return W4A8_ERR_WORKSPACE;
+    if (need > 0 && !workspace) return W4A8_ERR_NULL_PTR;
+    if (need > 0 && !aligned16(workspace)) return W4A8_ERR_ALIGNMENT;
+    w4a8_status_t d = check_device();
+    if (d != W4A8_OK) return d;
+    return hip_status(w4a8::launch_route(logits, in_type, T, E, k, renormalize, ids, weights,
+                                         offsets, rows, workspace, stream));
+}
+
+W4A8_EXPORT size_t w4a8_moe_workspace_size(int T, int E, int k, int H, int F) {
+    if (!valid_moe(T, E, k, H, F) || T == 0) return 0;
+    return w4a8::moe_workspace(T, k, H, F);
+}
+
+W4A8_EXPORT w4a8_status_t w4a8_moe(const void* X, int in_type, const int32_t* ids,
+                                   const float* weights, int T, int E, int k,
+                                   const uint8_t* wq13, const uint8_t* s13, const uint8_t* a13,
+                                   const float* sw13, const uint8_t* wq2, const uint8_t* s2,
+                                   const uint8_t* a2, const float* sw2, void* Y, int out_type,
+                                   int H, int F, int group, void* workspace,
+                                   size_t workspace_bytes, hipStream_t stream) {
+    if (!valid_in_type(in_type) || !valid_in_type(out_type)) return W4A8_ERR_UNSUPPORTED;
+    if (!valid_moe(T, E, k, H, F) || !valid_group(group)) return W4A8_ERR_SHAPE;
+    if (T == 0) return W4A8_OK;  // nothing to read or write
+    if (!X || !ids || !weights || !Y || !wq13 || !s13 || !a13 || !sw13 || !wq2 || !s2 || !a2 ||
+        !sw2)
+        return W4A8_ERR_NULL_PTR;
+    if (!aligned16(X) || !aligned16(Y) || !aligned16(wq13) || !aligned16(s13) ||
+        !aligned16(a13) || !aligned16(wq2) || !aligned16(s2) || !aligned16(a2))
+        return W4A8_ERR_ALIGNMENT;
+    if (!aligned4(ids) || !aligned4(weights) || !aligned4(sw13) || !aligned4(sw2))
+        return W4A8_ERR_ALIGNMENT;
+    if (workspace_bytes < w4a8_moe_workspace_size(T, E, k, H, F)) return W4A8_ERR_WORKSPACE;
+    if (!workspace) return W4A8_ERR_NULL_PTR;
+    if (!aligned16(workspace)) return W4A8_ERR_ALIGNMENT;
+    w4a8_status_t d = check_device();
+    if (d != W4A8_OK) return d;
+    return hip_status(w4a8::launch_moe(X, in_type, ids, weights, T, E, k,
+                                       w4a8::MoeWeights{wq13, s13, a13, sw13},
+                                       w4a8::MoeWeights{wq2, s2, a2, sw2}, Y, out_type, H, F,
+                                       group, workspace, stream));
+}
+
+namespace {
+
+// Workspace of gemm_lora: the INT8 rows and their scales, the adapters'
+// first products, the int32 sums, and the shared projection's own workspace.
+struct LoraLayout {
+    size_t xq, sx, v, acc, gemm, bytes;
+    LoraLayout(int M, int N, int K, int R) {
+        size_t o = 0;
+        auto take = [&](size_t n) {
+            const size_t at = o;
+            o += (n + 255) & ~(size_t)255;
+            return at;
+        };
+        xq = take((size_t)M * K);
+        sx = take((size_t)M * sizeof(float));
+        v = take((size_t)M * R * sizeof(float));
+        acc = take((size_t)M * N * sizeof(int));
+        gemm = take(w4a8_workspace_size(M, N, K, 0));
+        bytes = o;
+    }
+};
+
+}  // namespace
+
+W4A8_EXPORT size_t w4a8_gemm_lora_workspace_size(int M, int N, int K, int R) {
+    if (M <= 0 || N == 0 || !valid_nk(N, K) || !valid_extent(M, N, K) || !valid_rank(R)) return 0;
+    return LoraLayout(M, N, K, R).bytes;
+}
+
+W4A8_EXPORT w4a8_status_t w4a8_gemm_lora(const void* X, int in_type, const uint8_t* wq,
+                                         const uint8_t* s_u8, const uint8_t* a_u8,
+                                         const float* sw, const void* A, const void* B,
+                                         const float* scale, int n_adapters, int R,
+                                         const int32_t* adapter, void* Y, int M, int N, int K,
+                                         int group, void* workspace, size_t workspace_bytes,
+                                         hipStream_t stream) {
+    if (in_type != W4A8_IN_F16 && in_type != W4A8_IN_BF16) return W4A8_ERR_UNSUPPORTED;
+    if (M < 0 || !valid_nk(N, K) || !valid_group(group) || !valid_rank(R) || n_adapters < 0)
+        return W4A8_ERR_SHAPE;
+    if (!valid_extent(M, N, K)) return W4A8_ERR_SHAPE;
+    if (M == 0 || N == 0) return W4A8_OK;  // nothing to read or write
+    if (!X || !wq || !s_u8 || !a_u8 || !sw || !adapter || !Y) return W4A8_ERR_NULL_PTR;
+    if (n_adapters > 0 && (!A || !B || !scale)) return W4A8_ERR_NULL_PTR;
+    if (!aligned16(X) || !aligned16(wq) || !aligned16(s_u8) || !aligned16(a_u8) ||
+        !aligned16(Y) || !aligned16(A) || !aligned16(B))
+        return W4A8_ERR_ALIGNMENT;
+    if (!aligned4(sw) || !aligned4(scale) || !aligned4(adapter)) return W4A8_ERR_ALIGNMENT;
+    const LoraLayout lay(M, N, K, R);
+    if (workspace_bytes < lay.bytes) return W4A8_ERR_WORKSPACE;
+    if (!workspace) return W4A8_ERR_NULL_PTR;
+    if (!aligned16(workspace)) return W4A8_ERR_ALIGNMENT;
+    w4a8_status_t d = check_device();
+    if (d != W4A8_OK) return d;
+    uint8_t* ws = reinterpret_cast<uint8_t*>(workspace);
+    int8_t* xq = reinterpret_cast<int8_t*>(ws + lay.xq);
+    float* sx = reinterpret_cast<float*>(ws + lay.sx);
+    float* v = reinterpret_cast<float*>(ws + lay.v);
+    int* acc = reinterpret_cast<int*>(ws + lay.acc);
+    hipError_t e = w4a8::launch_act_int8(X, in_type, M, K, xq, sx, stream);
+    if (e != hipSuccess) return hip_status(e);
+    e = w4a8::launch_lora_shrink(X, in_type, A, adapter, scale, n_adapters, M, K, R, v, stream);
+    if (e != hipSuccess) return hip_status(e);
+    d = w4a8::gemm_entry(xq, sx, wq, s_u8, a_u8, sw, acc, W4A8_OUT_I32, M, N, K, group, 0,
+                         ws + lay.gemm, workspace_bytes - lay.gemm, false, stream);
+    if (d != W4A8_OK) return d;
+    return hip_status(w4a8::launch_lora_expand(acc, sx, sw, v, in_type, B, adapter, n_adapters, M,
+                                               N, R, Y, stream));
 }

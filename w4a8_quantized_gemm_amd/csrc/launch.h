@@ -129,4 +129,37 @@ hipError_t launch_w4fp8g_stream(const uint8_t* X, const float* sx, const uint8_t
 // device (looked up once per device); W4A8_NOALLOC_SCRATCH_BYTES long.
 hipError_t noalloc_scratch(void** ptr);
 
+// Top-k gating and grouping: one workgroup, or `blocks` workgroups of
+// `tokens` tokens with per-block counts in the workspace.
+struct RoutePlan {
+    int blocks;
+    int tokens;
+    size_t workspace;
+};
+RoutePlan plan_route(int T, int E, int k);
+hipError_t launch_route(const void* logits, int in_type, int T, int E, int k, int renorm,
+                        int* ids, float* weights, int* offsets, int* rows, void* workspace,
+                        hipStream_t st);
+
+// The packed weights of one product of every expert, laid end to end.
+struct MoeWeights {
+    const uint8_t* wq;
+    const uint8_t* s_u8;
+    const uint8_t* a_u8;
+    const float* sw;
+};
+size_t moe_workspace(int T, int k, int H, int F);
+hipError_t launch_moe(const void* X, int in_type, const int* ids, const float* weights, int T,
+                      int E, int k, const MoeWeights& w13, const MoeWeights& w2, void* Y,
+                      int out_type, int H, int F, int group, void* workspace, hipStream_t st);
+
+// The two products of the low-rank adapters: V [M][R] float32, and the
+// epilogue of a shared projection whose int32 sums lie in memory.
+hipError_t launch_lora_shrink(const void* X, int in_type, const void* A, const int* adapter,
+                              const float* scale, int n_adapters, int M, int K, int R, float* V,
+                              hipStream_t st);
+hipError_t launch_lora_expand(const int* acc, const float* sx, const float* sw, const float* V,
+                              int in_type, const void* B, const int* adapter, int n_adapters,
+                              int M, int N, int R, void* Y, hipStream_t st);
+
 }  // namespace w4a8
