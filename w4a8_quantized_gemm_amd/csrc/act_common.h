@@ -80,4 +80,62 @@ __device__ __forceinline__ float block_max(float m) {
     return m;
 }
 
+// Per-token quantisation of one row by a workgroup of TPB threads, the row
+// held in registers between the absolute maximum and the quantisation (rows
+// of at most 8 TPB CH elements), so it is read from memory once.  Q: 0 =
+// INT8 (qmax 127), 1 = e4m3.
+template <int IN, int Q, int CH, int TPB>
+__device__ __forceinline__ void quant_row_regs(const void* row, int K, uint8_t* Xq_row,
+                                               float* sx_row) {
+    const int n8 = K / 8;
+    Raw8<IN> c[CH];
+#pragma unroll
+    for (int j = 0; j < CH; ++j) {
+        const int i = threadIdx.x + TPB * j;
+        c[j] = i < n8 ? load_raw8<IN>(row, i) : Raw8<IN>{};
+    }
+    float m = 0.0f;
+#pragma unroll
+    for (int j = 0; j < CH; ++j) {
+        const Row8<IN> r = widen8<IN>(c[j]);  // zeros past the row end
+#pragma unroll
+        for (int e = 0; e < 8; ++e) m = fmaxf(m, fabsf(r.v[e]));
+    }
+    const float s = scale_of(block_max<TPB>(m), Q == 0 ? 127.0f : 448.0f);
+    if (threadIdx.x == 0) *sx_row = s;
+    uint2* out = reinterpret_cast<uint2*>(Xq_row);
+#pragma unroll
+    for (int j = 0; j < CH; ++j) {
+        const int i = threadIdx.x + TPB * j;
+        if (i >= n8) continue;
+        const Row8<IN> r = widen8<IN>(c[j]);
+        if constexpr (Q == 0) {
+            unsigned b[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) b[e] = (unsigned)(quant_sym(r.v[e], s, 127.0f) & 0xFF);
+            out[i] = uint2{b[0] | (b[1] << 8) | (b[2] << 16) | (b[3] << 24),
+                           b[4] | (b[5] << 8) | (b[6] << 16) | (b[7] << 24)};
+        } else {
+            // |x / s| <= 448 (1 + 2^-23) here, where the hardware conversion
+            // (nearest even) gives OCP e4m3's codes; a NaN quotient (NaN
+            // input) gets 0x7F whatever its sign
+            float t[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) t[e] = __fdiv_rn(r.v[e], s);
+            unsigned w[2];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int l = __builtin_amdgcn_cvt_pk_fp8_f32(t[4 * h], t[4 * h + 1], 0, false);
+                w[h] = (unsigned)__builtin_amdgcn_cvt_pk_fp8_f32(t[4 * h + 2], t[4 * h + 3], l,
+                                                                  true);
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (t[4 * h + e] != t[4 * h + e])
+                        w[h] = (w[h] & ~(0xFFu << (8 * e))) | (0x7Fu << (8 * e));
+            }
+            out[i] = uint2{w[0], w[1]};
+        }
+    }
+}
+
 }  // namespace w4a8

@@ -617,13 +617,13 @@ W4A8_EXPORT w4a8_status_t w4a8_gemm_lora(const void* X, int in_type, const uint8
     float* sx = reinterpret_cast<float*>(ws + lay.sx);
     float* v = reinterpret_cast<float*>(ws + lay.v);
     int* acc = reinterpret_cast<int*>(ws + lay.acc);
-    hipError_t e = w4a8::launch_act_int8(X, in_type, M, K, xq, sx, stream);
-    if (e != hipSuccess) return hip_status(e);
-    e = w4a8::launch_lora_shrink(X, in_type, A, adapter, scale, n_adapters, M, K, R, v, stream);
+    const w4a8::LoraArgs lora{v, B, adapter, n_adapters, R};
+    hipError_t e = w4a8::launch_lora_inputs(X, in_type, A, adapter, scale, n_adapters, M, K, R,
+                                            xq, sx, v, stream);
     if (e != hipSuccess) return hip_status(e);
     d = w4a8::gemm_entry(xq, sx, wq, s_u8, a_u8, sw, acc, W4A8_OUT_I32, M, N, K, group, 0,
                          ws + lay.gemm, workspace_bytes - lay.gemm, false, stream);
     if (d != W4A8_OK) return d;
-    return hip_status(w4a8::launch_lora_expand(acc, sx, sw, v, in_type, B, adapter, n_adapters, M,
-                                               N, R, Y, stream));
+    return hip_status(
+        w4a8::launch_lora_join(acc, 1, sx, sw, in_type, lora, M, N, Y, stream));
 }

@@ -153,13 +153,21 @@ hipError_t launch_moe(const void* X, int in_type, const int* ids, const float* w
                       int E, int k, const MoeWeights& w13, const MoeWeights& w2, void* Y,
                       int out_type, int H, int F, int group, void* workspace, hipStream_t st);
 
-// The two products of the low-rank adapters: V [M][R] float32, and the
-// epilogue of a shared projection whose int32 sums lie in memory.
-hipError_t launch_lora_shrink(const void* X, int in_type, const void* A, const int* adapter,
-                              const float* scale, int n_adapters, int M, int K, int R, float* V,
-                              hipStream_t st);
-hipError_t launch_lora_expand(const int* acc, const float* sx, const float* sw, const float* V,
-                              int in_type, const void* B, const int* adapter, int n_adapters,
-                              int M, int N, int R, void* Y, hipStream_t st);
+// Low-rank adapters: V [M][R] float32 = scale (X . A^T) of the rows that
+// select one, B [n_adapters][N][R] of in_type.
+struct LoraArgs {
+    const float* V;
+    const void* B;
+    const int* adapter;  // [M]
+    int n_adapters, R;
+};
+// Xq, sx = per-token INT8 of X, and V.
+hipError_t launch_lora_inputs(const void* X, int in_type, const void* A, const int* adapter,
+                              const float* scale, int n_adapters, int M, int K, int R,
+                              int8_t* Xq, float* sx, float* V, hipStream_t st);
+// The epilogue over `splits` parts of int32 sums in memory.
+hipError_t launch_lora_join(const int* acc, int splits, const float* sx, const float* sw,
+                            int in_type, const LoraArgs& lora, int M, int N, void* Y,
+                            hipStream_t st);
 
 }  // namespace w4a8
