@@ -562,9 +562,13 @@ W4A8_EXPORT w4a8_status_t w4a8_moe(const void* X, int in_type, const int32_t* id
 namespace {
 
 // Workspace of gemm_lora: the INT8 rows and their scales, the adapters'
-// first products, the int32 sums, and the shared projection's own workspace.
+// inner products, and, where the shared projection's kernel does not add the
+// adapters itself, its int32 sums (one part from the streamed kernel, the K
+// parts of a split tile plan).
 struct LoraLayout {
-    size_t xq, sx, v, acc, gemm, bytes;
+    size_t xq, sx, v, acc, bytes;
+    bool tiles;
+    w4a8::MfmaPlan plan{};
     LoraLayout(int M, int N, int K, int R) {
         size_t o = 0;
         auto take = [&](size_t n) {
@@ -575,8 +579,9 @@ struct LoraLayout {
         xq = take((size_t)M * K);
         sx = take((size_t)M * sizeof(float));
         v = take((size_t)M * R * sizeof(float));
-        acc = take((size_t)M * N * sizeof(int));
-        gemm = take(w4a8_workspace_size(M, N, K, 0));
+        tiles = use_mfma_tiles(M, N, K);
+        if (tiles) plan = w4a8::plan_w4a8_mfma(M, N, K);
+        acc = take(tiles ? plan.workspace : (size_t)M * N * sizeof(int));
         bytes = o;
     }
 };
@@ -621,9 +626,18 @@ W4A8_EXPORT w4a8_status_t w4a8_gemm_lora(const void* X, int in_type, const uint8
     hipError_t e = w4a8::launch_lora_inputs(X, in_type, A, adapter, scale, n_adapters, M, K, R,
                                             xq, sx, v, stream);
     if (e != hipSuccess) return hip_status(e);
-    d = w4a8::gemm_entry(xq, sx, wq, s_u8, a_u8, sw, acc, W4A8_OUT_I32, M, N, K, group, 0,
-                         ws + lay.gemm, workspace_bytes - lay.gemm, false, stream);
-    if (d != W4A8_OK) return d;
-    return hip_status(
-        w4a8::launch_lora_join(acc, 1, sx, sw, in_type, lora, M, N, Y, stream));
+    if (lay.tiles && lay.plan.splits == 1)
+        return hip_status(w4a8::launch_w4a8_mfma16_lora(xq, sx, wq, s_u8, a_u8, sw, in_type, lora,
+                                                        Y, M, N, K, group,
+                                                        lay.plan.mt16 ? lay.plan.mt16 : lay.plan.mt,
+                                                        stream));
+    if (lay.tiles)
+        e = w4a8::launch_w4a8_mfma16_partial(xq, wq, s_u8, a_u8, M, N, K, group, lay.plan, acc,
+                                             stream);
+    else
+        e = w4a8::launch_w4a8_stream(xq, sx, wq, s_u8, a_u8, sw, acc, W4A8_OUT_I32, M, N, K, group,
+                                     choose_stream(M, N, K, 0, true), stream);
+    if (e != hipSuccess) return hip_status(e);
+    return hip_status(w4a8::launch_lora_join(acc, lay.tiles ? lay.plan.splits : 1, sx, sw, in_type,
+                                             lora, M, N, Y, stream));
 }

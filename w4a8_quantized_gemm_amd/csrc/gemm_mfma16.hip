@@ -39,6 +39,7 @@
 #include <type_traits>
 
 #include "launch.h"
+#include "lora_common.h"
 #include "mfma_common.h"
 
 namespace w4a8 {
@@ -157,16 +158,131 @@ __device__ __forceinline__ void mfma16_drain(v4i (&acc)[RB][4]) {
 
 }  // namespace
 
+// Epilogue with low-rank adapters.  Accumulator layout as in the kernel's own
+// epilogue.  Row blocks are walked in a loop that is not unrolled, with a
+// uniform choice of the block's accumulators in front (their registers have
+// constant numbers): sixteen copies of the adapters' code would stream
+// through the instruction cache for every tile (4096 x 28672 x 8192, rank 16:
+// 864 us with the copies).  The rows' V, ids and scales lie in LDS where they
+// fit beside the staging block (ranks up to 72 or more).
+template <int MT, int LORA>
+__device__ __forceinline__ void mfma16_lora_epilogue(v4i (&acc)[MT / 16][4], uint8_t* lds,
+                                                     unsigned lds_bytes, float* sxs,
+                                                     const float* sw, const LoraArgs& lora, unsigned short* Y,
+                                                     int m0, int n0, int row_hi, int N) {
+    constexpr int RSTR = 64 * 2 + 16;  // padded row stride of the fp16 staging block
+    // LDS behind the staging blocks: per row and 32 ranks, 8 pieces of 16
+    // bytes (high and low operand parts of each 8 ranks), padded by one
+    constexpr unsigned VOFF = kWaves * 16 * RSTR;
+    constexpr unsigned VSTR = 8 * 16 + 16;
+    __shared__ int ids[MT];
+    __shared__ float backs[LORA == 1 ? MT * 4 : 1];                // [32 ranks][row]
+    __shared__ __attribute__((aligned(16))) float sws[kNT];  // the workgroup's channel scales
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int r = lane & 15, G = lane >> 4;
+    sws[tid] = sw[n0 - wave * kColsPerWave + tid];
+    const int ns = (lora.R + 31) / 32;
+    const bool v_in_lds = VOFF + (unsigned)(MT * ns) * VSTR <= lds_bytes;
+    ids[tid % MT] = lora_id(lora, m0 + tid % MT, m0 + tid % MT < row_hi);
+    if (v_in_lds) {  // four threads split a row's 32 ranks once for all waves
+        for (int i = tid; i < MT * 4 * ns; i += 256) {
+            const int row = (i >> 2) % MT, s = (i >> 2) / MT, k0 = 32 * s + 8 * (i & 3);
+            float v[8] = {};
+            if (m0 + row < row_hi && k0 < lora.R) {  // (rows without an adapter are not used)
+                const v4f* p = reinterpret_cast<const v4f*>(lora.V + (size_t)(m0 + row) * lora.R + k0);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) v[j] = p[j >> 2][j & 3];
+            }
+            const LoraV o = lora_split<LORA, 1, 2>(v);
+            v4i* dst = reinterpret_cast<v4i*>(lds + VOFF + (unsigned)(s * MT + row) * VSTR);
+            dst[2 * (i & 3)] = o.hi;
+            dst[2 * (i & 3) + 1] = o.lo;
+            if (LORA == 1 && (i & 3) == 0) backs[s * MT + row] = o.back;
+        }
+    }
+    __syncthreads();
+    uint8_t* stage = lds + wave * (16 * RSTR);
+    LoraHeld<MT == 256 ? 4 : 1> held;
+#pragma clang loop unroll(disable)
+    for (int rb = 0; rb < MT / 16; ++rb) {
+        // Read in assembly, so that the copies stay where they are: hoisted out
+        // of the loop they would need a register per accumulator, and the
+        // allocator, spilling parts of accumulators, has lost one.
+        v4i cur[4];
+        static_for<MT / 16>([&](auto i) {
+            if (rb == decltype(i)::value) {
+#pragma unroll
+                for (int cb = 0; cb < 4; ++cb)
+#pragma unroll
+                    for (int v = 0; v < 4; ++v) {
+                        int x;
+                        asm volatile("v_accvgpr_read_b32 %0, %1"
+                                     : "=v"(x)
+                                     : "a"(acc[decltype(i)::value][cb][v]));
+                        cur[cb][v] = x;
+                    }
+            }
+        });
+        const int row = 16 * rb + r;
+        const int id = ids[row];
+        const float sm = sxs[row];
+        v4f y[4];
+#pragma unroll
+        for (int cb = 0; cb < 4; ++cb) {
+            const v4f w =
+                *reinterpret_cast<const v4f*>(&sws[wave * kColsPerWave + 16 * cb + 4 * G]);
+#pragma unroll
+            for (int v = 0; v < 4; ++v) y[cb][v] = ((float)cur[cb][v] * sm) * w[v];
+        }
+        lora_add_held<LORA>(
+            lora, id, N, n0,
+            [&](int s) {
+                if (!v_in_lds) {
+                    float v[8];
+                    lora_load_v(lora, m0 + row, id >= 0, s, v);
+                    return lora_split<LORA>(v);
+                }
+                const v4i* p =
+                    reinterpret_cast<const v4i*>(lds + VOFF + (unsigned)(s * MT + row) * VSTR);
+                return LoraV{p[2 * G], p[2 * G + 1], LORA == 1 ? backs[s * MT + row] : 1.0f};
+            },
+            held, y);
+#pragma unroll
+        for (int cb = 0; cb < 4; ++cb) {
+            unsigned short h[4];
+#pragma unroll
+            for (int v = 0; v < 4; ++v) h[v] = f32_to_f16_bits(y[cb][v]);
+            *reinterpret_cast<uint2*>(stage + r * RSTR + (16 * cb + 4 * G) * 2) =
+                uint2{h[0] | ((unsigned)h[1] << 16), h[2] | ((unsigned)h[3] << 16)};
+        }
+        __builtin_amdgcn_s_waitcnt(0xc07f);  // lgkmcnt(0): this wave's LDS writes done
+        __builtin_amdgcn_wave_barrier();
+#pragma unroll
+        for (int w = 0; w < 2; ++w) {  // 16 rows of eight 16-byte pieces
+            const int q = lane + 64 * w, sr = q >> 3, piece = q & 7;
+            const int m = m0 + 16 * rb + sr;
+            const v4i val = *reinterpret_cast<const v4i*>(stage + sr * RSTR + piece * 16);
+            if (m < row_hi) store16_result<false>(Y + (size_t)m * N + n0 + piece * 8, val);
+        }
+        __builtin_amdgcn_s_waitcnt(0xc07f);
+        __builtin_amdgcn_wave_barrier();
+    }
+}
+
 // W8: the W8A8 comparison on this skeleton (no decode, no parameters).
 // 128-row tiles fit two workgroups per CU (128 accumulator registers per
 // lane, at most 128 others), 256-row tiles one; with K parts (KIN = 2) the
 // X tiles take 96 KiB of LDS, one workgroup per CU.
-template <int MT, int OUT, int GROUP, bool PARTIAL, bool W8, int KIN>
-__global__ __launch_bounds__(256, (MT == 128 && KIN == 1) ? 2 : 1) void w4a8_mfma16_kernel(
+// LORA (1: fp16, 2: bfloat16 adapters): the epilogue adds each row's low-rank
+// adapter to its scaled sums before the one rounding.
+template <int MT, int OUT, int GROUP, bool PARTIAL, bool W8, int KIN, int LORA>
+__device__ __forceinline__ void mfma16_body(
     const int8_t* __restrict__ X, const float* __restrict__ sx, const uint8_t* __restrict__ wq,
     const uint8_t* __restrict__ s_u8, const uint8_t* __restrict__ a_u8,
     const float* __restrict__ sw, void* __restrict__ Y, int* __restrict__ part, int M, int N,
-    int K, int tiles_n, int tiles_m, int splits, const int* __restrict__ offsets) {
+    int K, int tiles_n, int tiles_m, int splits, const int* __restrict__ offsets,
+    const LoraArgs& lora) {
+    static_assert(LORA == 0 || (OUT == 0 && !PARTIAL && !W8 && KIN == 1), "one rounding to fp16");
     static_assert(KIN == 1 || (KIN == 2 && MT == 128), "K parts: 128-row tiles only");
     constexpr int RB = MT / 16;        // 16-row blocks per wave
     constexpr int NWX = kWaves / KIN;  // waves per K part (sharing its X tiles)
@@ -394,6 +510,11 @@ __global__ __launch_bounds__(256, (MT == 128 && KIN == 1) ? 2 : 1) void w4a8_mfm
     // (final output, or this split's int32 partial).
     constexpr bool SCALED = (OUT == 0) && !PARTIAL;
     if (SCALED) sxs[tid % MT] = (m0 + tid % MT < row_hi) ? sx[m0 + tid % MT] : 0.0f;
+    if constexpr (LORA != 0) {
+        mfma16_lora_epilogue<MT, LORA>(acc, xs, 3 * XSTEP, sxs, sw, lora,
+                                       reinterpret_cast<unsigned short*>(Y), m0, n0, row_hi, N);
+        return;
+    }
     float swv[4][4];
 #pragma unroll
     for (int cb = 0; cb < 4; ++cb)
@@ -489,6 +610,28 @@ __global__ __launch_bounds__(256, (MT == 128 && KIN == 1) ? 2 : 1) void w4a8_mfm
             [&](int rb, int cb) { return fin[rb][cb]; });
 }
 
+template <int MT, int OUT, int GROUP, bool PARTIAL, bool W8, int KIN>
+__global__ __launch_bounds__(256, (MT == 128 && KIN == 1) ? 2 : 1) void w4a8_mfma16_kernel(
+    const int8_t* __restrict__ X, const float* __restrict__ sx, const uint8_t* __restrict__ wq,
+    const uint8_t* __restrict__ s_u8, const uint8_t* __restrict__ a_u8,
+    const float* __restrict__ sw, void* __restrict__ Y, int* __restrict__ part, int M, int N,
+    int K, int tiles_n, int tiles_m, int splits, const int* __restrict__ offsets) {
+    mfma16_body<MT, OUT, GROUP, PARTIAL, W8, KIN, 0>(X, sx, wq, s_u8, a_u8, sw, Y, part, M, N, K,
+                                                     tiles_n, tiles_m, splits, offsets,
+                                                     LoraArgs{});
+}
+
+// The unsplit fp16 kernel with the adapters in its epilogue.
+template <int MT, int GROUP, int LORA>
+__global__ __launch_bounds__(256, MT == 128 ? 2 : 1) void w4a8_mfma16_lora_kernel(
+    const int8_t* __restrict__ X, const float* __restrict__ sx, const uint8_t* __restrict__ wq,
+    const uint8_t* __restrict__ s_u8, const uint8_t* __restrict__ a_u8,
+    const float* __restrict__ sw, LoraArgs lora, void* __restrict__ Y, int M, int N, int K,
+    int tiles_n, int tiles_m) {
+    mfma16_body<MT, 0, GROUP, false, false, 1, LORA>(X, sx, wq, s_u8, a_u8, sw, Y, nullptr, M, N,
+                                                     K, tiles_n, tiles_m, 1, nullptr, lora);
+}
+
 template <int MT, int OUT, bool PARTIAL, bool W8, int KIN = 1>
 static void launch_tile16(const int8_t* X, const float* sx, const uint8_t* wq,
                           const uint8_t* s_u8, const uint8_t* a_u8, const float* sw, void* Y,
@@ -558,6 +701,55 @@ hipError_t launch_w4a8_mfma16(const int8_t* X, const float* sx, const uint8_t* w
                               int max_rows) {
     return run_mfma16<false>(X, sx, wq, s_u8, a_u8, sw, Y, out_type, M, N, K, group, plan,
                              workspace, st, offsets, E, max_rows);
+}
+
+hipError_t launch_w4a8_mfma16_partial(const int8_t* X, const uint8_t* wq, const uint8_t* s_u8,
+                                      const uint8_t* a_u8, int M, int N, int K, int group,
+                                      const MfmaPlan& plan, int* part, hipStream_t st) {
+    if (plan.mt == 256)
+        launch_tile16<256, 1, true, false>(X, nullptr, wq, s_u8, a_u8, nullptr, nullptr, part, M,
+                                           N, K, group, plan.splits, st, nullptr, 1, 0);
+    else
+        launch_tile16<128, 1, true, false>(X, nullptr, wq, s_u8, a_u8, nullptr, nullptr, part, M,
+                                           N, K, group, plan.splits, st, nullptr, 1, 0);
+    return hipGetLastError();
+}
+
+namespace {
+
+template <int MT, int GROUP, int LORA>
+void launch_tile16_lora(const int8_t* X, const float* sx, const uint8_t* wq, const uint8_t* s_u8,
+                        const uint8_t* a_u8, const float* sw, const LoraArgs& lora, void* Y, int M,
+                        int N, int K, hipStream_t st) {
+    const int tiles_n = N / kNT, tiles_m = (M + MT - 1) / MT;
+    hipLaunchKernelGGL((w4a8_mfma16_lora_kernel<MT, GROUP, LORA>), dim3(tiles_n * tiles_m),
+                       dim3(256), 0, st, X, sx, wq, s_u8, a_u8, sw, lora, Y, M, N, K, tiles_n,
+                       tiles_m);
+}
+
+}  // namespace
+
+hipError_t launch_w4a8_mfma16_lora(const int8_t* X, const float* sx, const uint8_t* wq,
+                                   const uint8_t* s_u8, const uint8_t* a_u8, const float* sw,
+                                   int in_type, const LoraArgs& lora, void* Y, int M, int N, int K,
+                                   int group, int mt, hipStream_t st) {
+#define T16_LORA(MT_, G_, L_) \
+    launch_tile16_lora<MT_, G_, L_>(X, sx, wq, s_u8, a_u8, sw, lora, Y, M, N, K, st)
+#define T16_LORA_TYPE(MT_, G_)             \
+    do {                                   \
+        if (in_type == 1) T16_LORA(MT_, G_, 1); \
+        else T16_LORA(MT_, G_, 2);         \
+    } while (0)
+    if (mt == 256) {
+        if (group == 64) T16_LORA_TYPE(256, 64);
+        else T16_LORA_TYPE(256, 128);
+    } else {
+        if (group == 64) T16_LORA_TYPE(128, 64);
+        else T16_LORA_TYPE(128, 128);
+    }
+#undef T16_LORA_TYPE
+#undef T16_LORA
+    return hipGetLastError();
 }
 
 hipError_t launch_w8a8_mfma16(const int8_t* X, const float* sx, const int8_t* wq8,

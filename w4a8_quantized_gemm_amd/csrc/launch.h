@@ -165,6 +165,15 @@ struct LoraArgs {
 hipError_t launch_lora_inputs(const void* X, int in_type, const void* A, const int* adapter,
                               const float* scale, int n_adapters, int M, int K, int R,
                               int8_t* Xq, float* sx, float* V, hipStream_t st);
+// The 16 x 16 x 64 tile kernel with the adapters in its epilogue (mt = 128 or
+// 256 rows, no K split), and its int32 partials alone (plan.splits > 1).
+hipError_t launch_w4a8_mfma16_lora(const int8_t* X, const float* sx, const uint8_t* wq,
+                                   const uint8_t* s_u8, const uint8_t* a_u8, const float* sw,
+                                   int in_type, const LoraArgs& lora, void* Y, int M, int N, int K,
+                                   int group, int mt, hipStream_t st);
+hipError_t launch_w4a8_mfma16_partial(const int8_t* X, const uint8_t* wq, const uint8_t* s_u8,
+                                      const uint8_t* a_u8, int M, int N, int K, int group,
+                                      const MfmaPlan& plan, int* part, hipStream_t st);
 // The epilogue over `splits` parts of int32 sums in memory.
 hipError_t launch_lora_join(const int* acc, int splits, const float* sx, const float* sw,
                             int in_type, const LoraArgs& lora, int M, int N, void* Y,

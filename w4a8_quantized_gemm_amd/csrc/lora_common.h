@@ -38,8 +38,9 @@ struct LoraV {
     float back;
 };
 
-// v: ranks 32 s + 8 G .. + 7 of row (lane % 16), G = lane / 16.
-template <int IN>
+// v: 8 of a row's 32 ranks; the lanes that hold the other 24 are this lane's
+// number with the bits X1 and X2 flipped.
+template <int IN, int X1 = 16, int X2 = 32>
 __device__ __forceinline__ LoraV lora_split(const float (&v)[8]) {
     LoraV o;
     unsigned h[8], l[8];
@@ -50,9 +51,9 @@ __device__ __forceinline__ LoraV lora_split(const float (&v)[8]) {
             const unsigned b = __builtin_bit_cast(unsigned, v[j]) & 0x7FFFFFFFu;
             m = b > m ? b : m;
         }
-        const unsigned m1 = __shfl_xor(m, 16, 64);
+        const unsigned m1 = __shfl_xor(m, X1, 64);
         m = m1 > m ? m1 : m;
-        const unsigned m2 = __shfl_xor(m, 32, 64);
+        const unsigned m2 = __shfl_xor(m, X2, 64);
         m = m2 > m ? m2 : m;
         // exponent field of the largest; far below float32's normal range
         // the elements may vanish (their products are below 2^-90)
@@ -63,7 +64,7 @@ __device__ __forceinline__ LoraV lora_split(const float (&v)[8]) {
         for (int j = 0; j < 8; ++j) {
             const float x = v[j] * to;
             const _Float16 a = (_Float16)x;
-            const float d = x - (float)a;
+            const float d = x - (float)a;  // NaN where a is infinite: no low part then
             const _Float16 b = (_Float16)(d == d ? d : 0.0f);
             h[j] = __builtin_bit_cast(unsigned short, a);
             l[j] = __builtin_bit_cast(unsigned short, b);
@@ -72,9 +73,9 @@ __device__ __forceinline__ LoraV lora_split(const float (&v)[8]) {
         o.back = 1.0f;
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-            h[j] = f32_to_bf16_bits(v[j]);
+            h[j] = __builtin_bit_cast(unsigned short, (__bf16)v[j]);  // to nearest even
             const float d = v[j] - __builtin_bit_cast(float, h[j] << 16);
-            l[j] = f32_to_bf16_bits(d == d ? d : 0.0f);  // hi infinite: lo 0
+            l[j] = __builtin_bit_cast(unsigned short, (__bf16)(d == d ? d : 0.0f));
         }
     }
     o.hi = v4i{(int)(h[0] | h[1] << 16), (int)(h[2] | h[3] << 16), (int)(h[4] | h[5] << 16),
@@ -116,56 +117,126 @@ __device__ __forceinline__ int lora_id(const LoraArgs& L, int m, bool live) {
     return a >= 0 && a < L.n_adapters ? a : -1;
 }
 
-// delta[c][v] for row (lane % 16), channel n0 + 16 c + 4 (lane / 16) + v, of
-// the 16 rows whose adapters are `id` (equal for the four lanes of a row).
-// Adapters are taken four at a time, so their operands are in flight
-// together; every 32 ranks are one pass.
-template <int IN, int NC>
-__device__ __forceinline__ void lora_block(const LoraArgs& L, int m, int id, int N, int n0,
-                                           v4f (&delta)[NC]) {
-    constexpr int BATCH = NC == 1 ? 4 : 1;
+// y[c] += the product of NC channel blocks for one adapter: bfloat16
+// accumulates onto y in the matrix core, fp16 is scaled back and added.
+// TILE: inside a tile kernel, whose accumulators fill the AGPRs.  There the
+// compiler would give these instructions AGPR operands too and move
+// accumulators out of their way (and, where it runs out of registers, has
+// stored an accumulator incompletely), so they are issued in assembly on
+// VGPRs: five wait states for the operands, the dependent halves four
+// instructions apart, and 20 wait states (see mfma_loop_exit_wait) before
+// anything reads the results or overwrites the operands.
+template <int IN>
+__device__ __forceinline__ void lora_mfma4_asm(const v4i (&b)[4], const LoraV& V, v4f (&t)[4]) {
+#define LORA_MFMA4_ASM(OP)                                                                       \
+    asm volatile("s_nop 4\n\t" OP " %0, %4, %8, %0\n\t" OP " %1, %5, %8, %1\n\t" OP           \
+                 " %2, %6, %8, %2\n\t" OP " %3, %7, %8, %3\n\t" OP " %0, %4, %9, %0\n\t" OP     \
+                 " %1, %5, %9, %1\n\t" OP " %2, %6, %9, %2\n\t" OP " %3, %7, %9, %3\n\t"         \
+                 "s_nop 7\n\ts_nop 7\n\ts_nop 3"                                                \
+                 : "+v"(t[0]), "+v"(t[1]), "+v"(t[2]), "+v"(t[3])                                \
+                 : "v"(b[0]), "v"(b[1]), "v"(b[2]), "v"(b[3]), "v"(V.lo), "v"(V.hi))
+    if constexpr (IN == 1)
+        LORA_MFMA4_ASM("v_mfma_f32_16x16x32_f16");
+    else
+        LORA_MFMA4_ASM("v_mfma_f32_16x16x32_bf16");
+#undef LORA_MFMA4_ASM
+}
+
+template <int IN, bool TILE, int NC>
+__device__ __forceinline__ void lora_mac(const v4i (&b)[NC], const LoraV& V, v4f (&y)[NC]) {
+    static_assert(!TILE || NC == 4, "four channel blocks");
+    v4f t[NC];
 #pragma unroll
-    for (int c = 0; c < NC; ++c) delta[c] = v4f{0, 0, 0, 0};
+    for (int c = 0; c < NC; ++c) t[c] = IN == 2 ? y[c] : v4f{0, 0, 0, 0};
+    if constexpr (TILE) {
+        lora_mfma4_asm<IN>(b, V, t);
+    } else {
+#pragma unroll
+        for (int c = 0; c < NC; ++c) t[c] = lora_mfma<IN>(b[c], V.lo, t[c]);
+#pragma unroll
+        for (int c = 0; c < NC; ++c) t[c] = lora_mfma<IN>(b[c], V.hi, t[c]);
+    }
+#pragma unroll
+    for (int c = 0; c < NC; ++c)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) y[c][q] = IN == 2 ? t[c][q] : fmaf(t[c][q], V.back, y[c][q]);
+}
+
+// y[c][v] += the adapter's product for row (lane % 16), channel
+// n0 + 16 c + 4 (lane / 16) + v, of the 16 rows whose adapters are `id`
+// (equal for the four lanes of a row); get_v(s) gives the row's operands of
+// the s-th 32 ranks.  Adapters are taken four at a time (one with several
+// channel blocks), so their operands are in flight together; every 32 ranks
+// are one pass.
+template <int IN, bool TILE, int NC, typename GetV>
+__device__ __forceinline__ void lora_add(const LoraArgs& L, int id, int N, int n0, GetV get_v,
+                                         v4f (&y)[NC]) {
+    constexpr int BATCH = NC == 1 ? 4 : 1;
     const unsigned any = (unsigned)__ballot(id >= 0) & 0xFFFFu;
     if (any == 0) return;
     for (int s = 0; 32 * s < L.R; ++s) {
-        float v[8];
-        lora_load_v(L, m, id >= 0, s, v);
-        LoraV V;
-        bool split = false;
+        const LoraV V = get_v(s);
         unsigned rest = any;
         while (rest) {
             int a[BATCH];
             v4i b[BATCH][NC];
-            unsigned left = rest;
 #pragma unroll
             for (int i = 0; i < BATCH; ++i) {
                 a[i] = -1;
-                if (left) {
-                    a[i] = __builtin_amdgcn_readlane(id, __builtin_ctz(left));
-                    left &= ~(unsigned)__ballot(id == a[i]);
+                if (rest) {
+                    a[i] = __builtin_amdgcn_readlane(id, __builtin_ctz(rest));
+                    rest &= ~(unsigned)__ballot(id == a[i]);
 #pragma unroll
                     for (int c = 0; c < NC; ++c) b[i][c] = lora_load_b(L, a[i], N, n0 + 16 * c, s);
                 }
             }
-            rest = left;
-            if (!split) {
-                V = lora_split<IN>(v);
-                split = true;
-            }
 #pragma unroll
             for (int i = 0; i < BATCH; ++i) {
                 if (a[i] < 0) continue;
+                v4f t[NC];
 #pragma unroll
-                for (int c = 0; c < NC; ++c) {
-                    v4f t = lora_mfma<IN>(b[i][c], V.lo, v4f{0, 0, 0, 0});
-                    t = lora_mfma<IN>(b[i][c], V.hi, t);
-                    if (id == a[i])
+                for (int c = 0; c < NC; ++c) t[c] = y[c];
+                lora_mac<IN, TILE>(b[i], V, t);
 #pragma unroll
-                        for (int q = 0; q < 4; ++q) delta[c][q] = fmaf(t[q], V.back, delta[c][q]);
-                }
+                for (int c = 0; c < NC; ++c)
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) y[c][q] = id == a[i] ? t[c][q] : y[c][q];
             }
         }
+    }
+}
+
+// B operands of one adapter held in registers over consecutive row blocks,
+// for adapters of at most 32 NS ranks.
+template <int NS>
+struct LoraHeld {
+    v4i b[NS][4];
+    int a = -1;
+};
+
+// lora_add for the tile kernels, which walk many row blocks of the same
+// channels: a block whose rows all select one adapter (prompts: almost every
+// block) uses the held operands and needs no select.
+template <int IN, int NS, typename GetV>
+__device__ __forceinline__ void lora_add_held(const LoraArgs& L, int id, int N, int n0, GetV get_v,
+                                              LoraHeld<NS>& held, v4f (&y)[4]) {
+    const int a = __builtin_amdgcn_readfirstlane(id);
+    if (a < 0 || L.R > 32 * NS || __ballot(id == a) != ~0ull) {
+        lora_add<IN, true>(L, id, N, n0, get_v, y);
+        return;
+    }
+    if (held.a != a) {
+        held.a = a;
+#pragma unroll
+        for (int s = 0; s < NS; ++s)
+            if (32 * s < L.R)
+#pragma unroll
+                for (int c = 0; c < 4; ++c) held.b[s][c] = lora_load_b(L, a, N, n0 + 16 * c, s);
+    }
+#pragma unroll
+    for (int s = 0; s < NS; ++s) {
+        if (32 * s >= L.R) continue;
+        lora_mac<IN, true>(held.b[s], get_v(s), y);
     }
 }
 
