@@ -563,12 +563,14 @@ namespace {
 
 // Workspace of gemm_lora: the INT8 rows and their scales, the adapters'
 // inner products, and, where the shared projection's kernel does not add the
-// adapters itself, its int32 sums (one part from the streamed kernel, the K
-// parts of a split tile plan).
+// adapters itself, its int32 sums (the K parts of a split tile plan; one part
+// from the streamed kernel for K so long that the group parameters do not
+// fit in LDS, at the smaller group size, which the size has to cover).
 struct LoraLayout {
     size_t xq, sx, v, acc, bytes;
     bool tiles;
     w4a8::MfmaPlan plan{};
+    w4a8::StreamCfg stream{};
     LoraLayout(int M, int N, int K, int R) {
         size_t o = 0;
         auto take = [&](size_t n) {
@@ -580,8 +582,14 @@ struct LoraLayout {
         sx = take((size_t)M * sizeof(float));
         v = take((size_t)M * R * sizeof(float));
         tiles = use_mfma_tiles(M, N, K);
-        if (tiles) plan = w4a8::plan_w4a8_mfma(M, N, K);
-        acc = take(tiles ? plan.workspace : (size_t)M * N * sizeof(int));
+        if (tiles) {
+            plan = w4a8::plan_w4a8_mfma(M, N, K);
+            acc = take(plan.workspace);
+        } else {
+            stream = choose_stream(M, N, K, 0, true);
+            const bool fits = w4a8::stream_lora_fits(stream, K, 64);
+            acc = take(fits ? 0 : (size_t)M * N * sizeof(int));
+        }
         bytes = o;
     }
 };
@@ -631,12 +639,15 @@ W4A8_EXPORT w4a8_status_t w4a8_gemm_lora(const void* X, int in_type, const uint8
                                                         Y, M, N, K, group,
                                                         lay.plan.mt16 ? lay.plan.mt16 : lay.plan.mt,
                                                         stream));
+    if (!lay.tiles && w4a8::stream_lora_fits(lay.stream, K, group))
+        return hip_status(w4a8::launch_w4a8_stream_lora(xq, sx, wq, s_u8, a_u8, sw, in_type, lora,
+                                                        Y, M, N, K, group, lay.stream, stream));
     if (lay.tiles)
         e = w4a8::launch_w4a8_mfma16_partial(xq, wq, s_u8, a_u8, M, N, K, group, lay.plan, acc,
                                              stream);
     else
         e = w4a8::launch_w4a8_stream(xq, sx, wq, s_u8, a_u8, sw, acc, W4A8_OUT_I32, M, N, K, group,
-                                     choose_stream(M, N, K, 0, true), stream);
+                                     lay.stream, stream);
     if (e != hipSuccess) return hip_status(e);
     return hip_status(w4a8::launch_lora_join(acc, lay.tiles ? lay.plan.splits : 1, sx, sw, in_type,
                                              lora, M, N, Y, stream));

@@ -174,6 +174,13 @@ hipError_t launch_w4a8_mfma16_lora(const int8_t* X, const float* sx, const uint8
 hipError_t launch_w4a8_mfma16_partial(const int8_t* X, const uint8_t* wq, const uint8_t* s_u8,
                                       const uint8_t* a_u8, int M, int N, int K, int group,
                                       const MfmaPlan& plan, int* part, hipStream_t st);
+// The streamed kernel with the adapters in its epilogue, where the parameters
+// of its tiles fit in LDS (more groups never fit where fewer do not).
+bool stream_lora_fits(StreamCfg cfg, int K, int group);
+hipError_t launch_w4a8_stream_lora(const int8_t* X, const float* sx, const uint8_t* wq,
+                                   const uint8_t* s_u8, const uint8_t* a_u8, const float* sw,
+                                   int in_type, const LoraArgs& lora, void* Y, int M, int N, int K,
+                                   int group, StreamCfg cfg, hipStream_t st);
 // The epilogue over `splits` parts of int32 sums in memory.
 hipError_t launch_lora_join(const int* acc, int splits, const float* sx, const float* sw,
                             int in_type, const LoraArgs& lora, int M, int N, void* Y,

@@ -76,140 +76,148 @@ __global__ __launch_bounds__(1024) void lora_inputs_kernel(
     shrink_row<IN>(X, A, m, a, scale[a], K, R, r0, V);
 }
 
-// INT8 of one row by one wave, the row in registers (K <= 512 CH): no barrier.
-template <int IN, int CH>
-__device__ __forceinline__ void quant_row_wave(const void* row, int K, uint8_t* xq, float* sx) {
-    const int lane = threadIdx.x & 63, n8 = K / 8;
+// INT8 of the rows of one workgroup of 16 waves: WPR waves a row, its elements
+// in registers (K <= 4096 WPR), maxima joined through LDS.
+template <int IN, int WPR>
+__device__ __forceinline__ void quant_rows16(const void* X, long long row0, int M, int K,
+                                             uint8_t* Xq, float* sx) {
+    constexpr int CH = 8;
+    __shared__ float part[16];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const long long m = row0 + wave / WPR;
+    const int first = (wave % WPR) * 64 * CH + lane, n8 = K / 8;
+    const uint8_t* row = reinterpret_cast<const uint8_t*>(X) + m * K * 2;
     Raw8<IN> c[CH];
-    float m = 0.0f;
+    float mx = 0.0f;
 #pragma unroll
     for (int j = 0; j < CH; ++j) {
-        const int i = lane + 64 * j;
-        c[j] = i < n8 ? load_raw8<IN>(row, i) : Raw8<IN>{};
+        const int i = first + 64 * j;
+        c[j] = m < M && i < n8 ? load_raw8<IN>(row, i) : Raw8<IN>{};
     }
 #pragma unroll
     for (int j = 0; j < CH; ++j) {
         const Row8<IN> v = widen8<IN>(c[j]);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) m = fmaxf(m, fabsf(v.v[e]));
+        for (int e = 0; e < 8; ++e) mx = fmaxf(mx, fabsf(v.v[e]));
         // a new definition, or the widened elements stay alive for the codes
         asm volatile("" : "+v"(c[j].w[0]));
     }
-    m = __builtin_bit_cast(float, wave_reduce(__builtin_bit_cast(unsigned, m), MaxU32{}));
-    const float s = scale_of(m, 127.0f), inv = __fdiv_rn(1.0f, s);
-    if (lane == 0) *sx = s;
+    mx = __builtin_bit_cast(float, wave_reduce(__builtin_bit_cast(unsigned, mx), MaxU32{}));
+    if constexpr (WPR > 1) {
+        if (lane == 0) part[wave] = mx;
+        __syncthreads();
+#pragma unroll
+        for (int w = 0; w < WPR; ++w) mx = fmaxf(mx, part[wave / WPR * WPR + w]);
+    }
+    if (m >= M) return;
+    const float s = scale_of(mx, 127.0f), inv = __fdiv_rn(1.0f, s);
+    if (first == 0) sx[m] = s;
 #pragma unroll
     for (int j = 0; j < CH; ++j) {
-        const int i = lane + 64 * j;
+        const int i = first + 64 * j;
         if (i >= n8) continue;
         const Row8<IN> v = widen8<IN>(c[j]);
-        reinterpret_cast<uint2*>(xq)[i] =
+        reinterpret_cast<uint2*>(Xq + m * K)[i] =
             uint2{quant4_fast(v.v[0], v.v[1], v.v[2], v.v[3], s, inv),
                   quant4_fast(v.v[4], v.v[5], v.v[6], v.v[7], s, inv)};
     }
 }
 
-// Large calls, workgroups of eight waves: the first ceil(M / 16) take the
-// inner product of 16 rows, the others quantise a row per wave (CH > 0); the
+// Large calls, workgroups of 16 waves: the first ceil(M / 16) take the inner
+// product of 16 rows, the others quantise 16 / WPR rows each (WPR > 0); the
 // two read X within a few microseconds of each other, so once from HBM.
-// Inner product: wave w takes the 128-wide K-tiles w, w + 8, ...  Matrix
-// instructions 16 x 16 x 32 take A as the first and X as the
-// second operand (lane (r, G): rank / row r, columns 8 G .. + 7 of a 32-wide
-// step).  Rows of different adapters run one pass per adapter that occurs
-// among them, each row keeping its own (a select).  RT blocks of 16 ranks
-// share a pass.
-template <int IN, int CH, int RT>
-__global__ __launch_bounds__(512, 4) void lora_rows_kernel(
+// Inner product: wave w takes the 64-wide K-tiles w, w + 16, ...  Matrix
+// instructions 16 x 16 x 32 take A as the first and X as the second operand
+// (lane (r, G): rank / row r, columns 8 G .. + 7 of a 32-wide step).  The
+// work of a block of rows is a list of jobs, one per adapter that occurs
+// among the rows and 16 of its ranks; a pass over K takes two jobs, and every
+// row keeps its own adapter's (a select).  The passes are bound by the cache:
+// every block of 16 rows reads its adapters' A again (2048 x 4096, rank 32:
+// 12 us without adapters, 16 with one, 27 with two per block; more loads in
+// flight and other column orders change nothing).
+template <int IN, int WPR>
+__global__ __launch_bounds__(1024, 8) void lora_rows_kernel(
     const void* __restrict__ X, const void* __restrict__ A, const int* __restrict__ adapter,
     const float* __restrict__ scale, int n_adapters, int M, int K, int R,
     uint8_t* __restrict__ Xq, float* __restrict__ sx, float* __restrict__ V) {
     const int blocks = (M + 15) / 16;
-    if constexpr (CH > 0) {
+    if constexpr (WPR > 0) {
         if ((int)blockIdx.x >= blocks) {
-            const size_t b = (size_t)(blockIdx.x - blocks) * 8 + (threadIdx.x >> 6);
-            if (b < (size_t)M)
-                quant_row_wave<IN, CH>(reinterpret_cast<const uint8_t*>(X) + b * K * 2, K,
-                                       Xq + b * K, sx + b);
+            quant_rows16<IN, WPR>(X, (long long)(blockIdx.x - blocks) * (16 / WPR), M, K, Xq, sx);
             return;
         }
     }
-    __shared__ __attribute__((aligned(16))) float red[8 * RT * 256];
+    __shared__ __attribute__((aligned(16))) float red[16 * 2 * 256];
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int r = lane & 15, G = lane >> 4, KT = K / 128;
+    const int r = lane & 15, G = lane >> 4, KT = K / 64;
     const int m = blockIdx.x * 16 + r;
     const bool live = m < M;
     const int id = live ? adapter[m] : -1;
     const uint8_t* x = reinterpret_cast<const uint8_t*>(X) + ((size_t)(live ? m : 0) * K + 8 * G) * 2;
     unsigned rest = (unsigned)__ballot(id >= 0 && id < n_adapters) & 0xFFFFu;
-    struct Tile {
-        v4i x[4], a[RT][4];
+    struct Job {
+        int a, r0;
+        unsigned rows;  // 0: no job
     };
-    while (rest) {
-        const int a = __builtin_amdgcn_readlane(id, __builtin_ctz(rest));
-        const unsigned mine = (unsigned)__ballot(id == a) & 0xFFFFu;
-        rest &= ~mine;
-        const float sc = scale[a];
-        for (int r0 = 0; r0 < R; r0 += 16 * RT) {
-            v4f acc[RT];
-            const uint8_t* ap[RT];
-            bool on[RT];
-#pragma unroll
-            for (int q = 0; q < RT; ++q) {
-                acc[q] = v4f{0, 0, 0, 0};
-                const int rr = r0 + 16 * q + r;
-                on[q] = rr < R;
-                ap[q] = reinterpret_cast<const uint8_t*>(A) +
-                        (((size_t)a * R + (on[q] ? rr : 0)) * K + 8 * G) * 2;
+    Job at{-1, R, 0};
+    auto next = [&]() {
+        at.r0 += 16;
+        if (at.r0 >= R) {
+            at.rows = 0;
+            if (rest) {
+                at.a = __builtin_amdgcn_readlane(id, __builtin_ctz(rest));
+                at.rows = (unsigned)__ballot(id == at.a) & 0xFFFFu;
+                at.r0 = 0;
+                rest &= ~at.rows;
             }
-            auto load = [&](int kt, Tile& t) {
+        }
+        return at;
+    };
+    for (;;) {
+        Job job[2];
+        job[0] = next();
+        if (job[0].rows == 0) return;
+        job[1] = next();
+        const bool both = job[1].rows != 0;
+        v4f acc[2] = {v4f{0, 0, 0, 0}, v4f{0, 0, 0, 0}};
+        const uint8_t* ap[2];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const size_t o = ((size_t)kt * 128 + 32 * i) * 2;
-                    t.x[i] = load16(x + o);  // a row past the end repeats row 0: not kept
+        for (int q = 0; q < 2; ++q) {  // ranks past R repeat the last: not kept
+            const int rr = min(job[q].r0 + r, R - 1);
+            ap[q] = reinterpret_cast<const uint8_t*>(A) +
+                    (((size_t)job[both ? q : 0].a * R + (both || q == 0 ? rr : 0)) * K + 8 * G) * 2;
+        }
+        for (int kt = wave; kt < KT; kt += 16) {
+            v4i xv[2], av[2][2];
 #pragma unroll
-                    for (int q = 0; q < RT; ++q) t.a[q][i] = load16(ap[q] + o);
-                }
-            };
-            auto use = [&](const Tile& t) {
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-#pragma unroll
-                    for (int q = 0; q < RT; ++q) acc[q] = lora_mfma<IN>(t.a[q][i], t.x[i], acc[q]);
-            };
-            if constexpr (RT == 1) {  // two tiles in flight
-                Tile t0, t1;
-                int kt = wave;
-                if (kt < KT) load(kt, t0);
-                for (; kt + 8 < KT; kt += 16) {
-                    load(kt + 8, t1);
-                    use(t0);
-                    if (kt + 16 < KT) load(kt + 16, t0);
-                    use(t1);
-                }
-                if (kt < KT) use(t0);
-            } else {  // (two would not fit 128 registers: four waves per SIMD hide the rest)
-                for (int kt = wave; kt < KT; kt += 8) {
-                    Tile t;
-                    load(kt, t);
-                    use(t);
-                }
+            for (int i = 0; i < 2; ++i) {
+                const size_t o = ((size_t)kt * 64 + 32 * i) * 2;
+                xv[i] = load16(x + o);  // a row past the end repeats row 0: not kept
+                av[0][i] = load16(ap[0] + o);
+                if (both) av[1][i] = load16(ap[1] + o);
             }
-            __syncthreads();  // the previous pass's sums have been read
 #pragma unroll
-            for (int q = 0; q < RT; ++q)
-                *reinterpret_cast<v4f*>(&red[((wave * RT + q) * 64 + lane) * 4]) = acc[q];
-            __syncthreads();
-            // element e of a rank block: lane e / 4 (row lane % 16), rank 4 (lane / 16) + e % 4
-            for (int e = tid; e < RT * 256; e += 512) {
-                float s = 0.0f;
-#pragma unroll
-                for (int w = 0; w < 8; ++w) s += red[w * RT * 256 + e];
-                const int l = (e & 255) >> 2, row = l & 15;
-                const int rank = r0 + 16 * (e >> 8) + 4 * (l >> 4) + (e & 3);
-                if (rank < R && ((mine >> row) & 1))
-                    V[((size_t)blockIdx.x * 16 + row) * R + rank] = s * sc;
+            for (int i = 0; i < 2; ++i) {
+                acc[0] = lora_mfma<IN>(av[0][i], xv[i], acc[0]);
+                if (both) acc[1] = lora_mfma<IN>(av[1][i], xv[i], acc[1]);
             }
+        }
+        __syncthreads();  // the previous pass's sums have been read
+#pragma unroll
+        for (int q = 0; q < 2; ++q)
+            *reinterpret_cast<v4f*>(&red[((wave * 2 + q) * 64 + lane) * 4]) = acc[q];
+        __syncthreads();
+        // element e of a job: lane e / 4 (row lane % 16), rank 4 (lane / 16) + e % 4
+        if (tid < 512) {
+            const Job j = tid < 256 ? job[0] : job[1];
+            float s = 0.0f;
+#pragma unroll
+            for (int w = 0; w < 16; ++w) s += red[w * 512 + tid];
+            const int l = (tid & 255) >> 2, row = l & 15;
+            const int rank = j.r0 + 4 * (l >> 4) + (tid & 3);
+            if (((j.rows >> row) & 1) && rank < R)
+                V[((size_t)blockIdx.x * 16 + row) * R + rank] = s * scale[j.a];
         }
     }
 }
@@ -277,22 +285,17 @@ hipError_t inputs_run(const void* X, const void* A, const int* adapter, const fl
     if (M >= 512) {
         // without adapters only the rows are quantised
         const int blocks = (M + 15) / 16;
-        if (K > 8192 || n_adapters == 0) {
+        if (K > 16384 || n_adapters == 0) {
             hipError_t e = launch_act_int8(X, IN, M, K, Xq, sx, st);
             if (e != hipSuccess || n_adapters == 0) return e;
         }
-#define ROWS(CH, RT)                                                                         \
-    hipLaunchKernelGGL((lora_rows_kernel<IN, CH, RT>), dim3(blocks + (CH > 0 ? (M + 7) / 8 : 0)), dim3(512), \
-                       0, st, X, A, adapter, scale, n_adapters, M, K, R, q, sx, V)
-#define ROWS_RT(CH)                \
-    do {                           \
-        if (R <= 16) ROWS(CH, 1);  \
-        else ROWS(CH, 2);          \
-    } while (0)
-        if (K <= 4096) ROWS_RT(8);
-        else if (K <= 8192) ROWS_RT(16);
-        else ROWS_RT(0);
-#undef ROWS_RT
+#define ROWS(WPR, ROWS_PER)                                                                      \
+    hipLaunchKernelGGL((lora_rows_kernel<IN, WPR>), dim3(blocks + ROWS_PER), dim3(1024), 0, st, X, \
+                       A, adapter, scale, n_adapters, M, K, R, q, sx, V)
+        if (K <= 4096) ROWS(1, (M + 15) / 16);
+        else if (K <= 8192) ROWS(2, (M + 7) / 8);
+        else if (K <= 16384) ROWS(4, (M + 3) / 4);
+        else ROWS(0, 0);
 #undef ROWS
         return hipGetLastError();
     }
