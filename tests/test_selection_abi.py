@@ -37,10 +37,10 @@ def test_route_refusals():
 
 def test_route_workspace_size():
     size = lib.w4a8_route_workspace_size
-    assert size(0, 8, 2) == 0 and size(1, 8, 2) == 0 and size(64, 512, 16) == 0
+    assert size(0, 8, 2) == 0 and size(1, 8, 2) == 0 and size(16, 512, 16) == 0
     assert size(-1, 8, 2) == 0 and size(1000, 0, 1) == 0 and size(1000, 8, 9) == 0
     for T in (65, 1000, 16384, 16385, 100000, (1 << 31) // 64 - 1):
-        assert 0 < size(T, 64, 6) <= 256 * 64 * 4
+        assert 0 < size(T, 64, 6) <= 512 * 64 * 4
 
 
 def moe(X=A, it=1, ids=A, w=A, T=4, E=8, k=2, wq13=A, s13=A, a13=A, sw13=A, wq2=A, s2=A, a2=A,

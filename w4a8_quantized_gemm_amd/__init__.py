@@ -11,6 +11,7 @@ below take torch tensors, check dtypes/devices/contiguity, and raise
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 
@@ -465,8 +466,15 @@ def gemm_w8a8(Xq, sx, packed, out_type: int = OUT_F16, splitk: int = 0, out=None
 # are allocated on the stream the call runs on.
 
 def _ready(t, dtype, shape, device, name):
-    """A contiguous tensor of this type and shape on this device."""
-    torch = _torch()
+    """A contiguous tensor of this type and shape (a tuple) on this device.
+    These calls take microseconds on the GPU, so the check is one expression
+    and the reason is looked for only when it fails."""
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape
+            and t.device == device and t.is_contiguous()):
+        _not_ready(t, dtype, shape, device, name)
+
+
+def _not_ready(t, dtype, shape, device, name):
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if tuple(t.shape) != tuple(shape):
@@ -475,19 +483,20 @@ def _ready(t, dtype, shape, device, name):
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if t.device != device:
         raise ValueError(f"{name} must be on {device}, got {t.device}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
+    raise ValueError(f"{name} must be contiguous")
 
 
-def _float_type(t, name, types=("float32", "float16", "bfloat16")):
-    torch = _torch()
+_FLOAT_TYPES = {torch.float32: IN_F32, torch.float16: IN_F16, torch.bfloat16: IN_BF16}
+_HALF_TYPES = {torch.float16: IN_F16, torch.bfloat16: IN_BF16}
+
+
+def _float_type(t, name, types=_FLOAT_TYPES):
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    codes = {"float32": IN_F32, "float16": IN_F16, "bfloat16": IN_BF16}
-    for n in types:
-        if t.dtype == getattr(torch, n):
-            return codes[n]
-    raise TypeError(f"{name} must be one of {', '.join(types)}, got {t.dtype}")
+    code = types.get(t.dtype)
+    if code is None:
+        raise TypeError(f"{name} must be one of {', '.join(map(str, types))}, got {t.dtype}")
+    return code
 
 
 def _on_gpu(t, name):
@@ -497,35 +506,23 @@ def _on_gpu(t, name):
         raise ValueError(f"{name} must be a 2-D tensor")
 
 
-class _Launch:
-    """The device and stream of one call; tensors allocated inside belong to
-    that stream."""
+_HERE = contextlib.nullcontext()
 
-    def __init__(self, device, stream):
-        torch = _torch()
-        if stream is not None and stream.device != device:
+
+def _context(device, stream):
+    """Context of a call: the tensors' device current, and its allocations on
+    the stream it runs on."""
+    if stream is not None:
+        if stream.device != device:
             raise ValueError(f"stream is on {stream.device}, the tensors on {device}")
-        self._ctx = None
-        if stream is not None:
-            self._ctx = torch.cuda.stream(stream)
-        elif torch.cuda.current_device() != device.index:
-            self._ctx = torch.cuda.device(device)
-        self._device, self._stream = device, stream
-
-    def __enter__(self):
-        if self._ctx is not None:
-            self._ctx.__enter__()
-        s = self._stream or _torch().cuda.current_stream(self._device)
-        return ctypes.c_void_p(s.cuda_stream)
-
-    def __exit__(self, *exc):
-        if self._ctx is not None:
-            self._ctx.__exit__(*exc)
+        return torch.cuda.stream(stream)
+    if torch.cuda.current_device() != device.index:
+        return torch.cuda.device(device)
+    return _HERE
 
 
 def _workspace(workspace, need, device):
     """(tensor, bytes) of the caller's workspace, or a new one."""
-    torch = _torch()
     if workspace is None:
         workspace = torch.empty(need, dtype=torch.uint8, device=device) if need else None
     elif workspace.device != device:
@@ -536,7 +533,6 @@ def _workspace(workspace, need, device):
 
 
 def _packed_ready(p, keys, E, device, name):
-    torch = _torch()
     N, K, g = p["N"], p["K"], p["group"]
     sizes = {"wq": N * K // 2, "s_u8": N * K // g, "a_u8": N * K // g, "sw": N}
     for k in keys:
@@ -557,7 +553,6 @@ def route(logits, k: int, renormalize: bool = True, out=None, workspace=None, st
     t*k + j by expert, -1 behind the last): ids and weights are moe()'s,
     offsets and X[rows // k] gemm_grouped()'s.  `out`: such a dict to write
     into."""
-    torch = _torch()
     it = _float_type(logits, "logits")
     _on_gpu(logits, "logits")
     T, E = logits.shape
@@ -565,7 +560,7 @@ def route(logits, k: int, renormalize: bool = True, out=None, workspace=None, st
     _ready(logits, logits.dtype, (T, E), dev, "logits")
     if not isinstance(k, int) or not 1 <= k <= min(E, MAX_TOPK):
         raise ValueError(f"k must be an integer in [1, {min(E, MAX_TOPK)}], got {k}")
-    with _Launch(dev, stream) as st:
+    with _context(dev, stream):
         if out is None:
             out = {"ids": torch.empty((T, k), dtype=torch.int32, device=dev),
                    "weights": torch.empty((T, k), dtype=torch.float32, device=dev),
@@ -579,7 +574,8 @@ def route(logits, k: int, renormalize: bool = True, out=None, workspace=None, st
         ws, ws_bytes = _workspace(workspace, route_workspace_size(T, E, k), dev)
         _check(lib.w4a8_route(_ptr(logits), it, T, E, k, int(bool(renormalize)),
                               _ptr(out["ids"]), _ptr(out["weights"]), _ptr(out["offsets"]),
-                              _ptr(out["rows"]), _ptr(ws), ws_bytes, st), "w4a8_route")
+                              _ptr(out["rows"]), _ptr(ws), ws_bytes,
+                              _stream()), "w4a8_route")
     return out
 
 
@@ -594,7 +590,6 @@ def moe(X, ids, weights, w13, w2, out=None, workspace=None, stream=None):
     (from route, or any; an id outside [0, E) is no expert); w13 and w2 from
     pack_experts on [E][2F][H] (gate rows, then up rows) and [E][H][F].
     Returns Y [T][H] in X's type, or writes into `out` (any of the three)."""
-    torch = _torch()
     it = _float_type(X, "X")
     _on_gpu(X, "X")
     T, H = X.shape
@@ -614,7 +609,7 @@ def moe(X, ids, weights, w13, w2, out=None, workspace=None, stream=None):
     _ready(weights, torch.float32, (T, k), dev, "weights")
     for p, name in ((w13, "w13"), (w2, "w2")):
         _packed_ready(p, ("wq", "s_u8", "a_u8", "sw"), E, dev, name)
-    with _Launch(dev, stream) as st:
+    with _context(dev, stream):
         if out is None:
             out = torch.empty((T, H), dtype=X.dtype, device=dev)
         ot = _float_type(out, "out")
@@ -623,7 +618,8 @@ def moe(X, ids, weights, w13, w2, out=None, workspace=None, stream=None):
         _check(lib.w4a8_moe(_ptr(X), it, _ptr(ids), _ptr(weights), T, E, k, _ptr(w13["wq"]),
                             _ptr(w13["s_u8"]), _ptr(w13["a_u8"]), _ptr(w13["sw"]),
                             _ptr(w2["wq"]), _ptr(w2["s_u8"]), _ptr(w2["a_u8"]), _ptr(w2["sw"]),
-                            _ptr(out), ot, H, F, g, _ptr(ws), ws_bytes, st), "w4a8_moe")
+                            _ptr(out), ot, H, F, g, _ptr(ws), ws_bytes,
+                              _stream()), "w4a8_moe")
     return out
 
 
@@ -638,8 +634,7 @@ def gemm_lora(X, packed, lora, adapter, out=None, workspace=None, stream=None):
     X: [M][K] float16 or bfloat16, not quantised; lora: dict of A [n][R][K],
     B [n][N][R] in X's type and scale float32 [n]; adapter: int32 [M], values
     outside [0, n) select none."""
-    torch = _torch()
-    it = _float_type(X, "X", ("float16", "bfloat16"))
+    it = _float_type(X, "X", _HALF_TYPES)
     _on_gpu(X, "X")
     M, K = X.shape
     dev = X.device
@@ -656,7 +651,7 @@ def gemm_lora(X, packed, lora, adapter, out=None, workspace=None, stream=None):
     _ready(lora["scale"], torch.float32, (n,), dev, "lora['scale']")
     _ready(adapter, torch.int32, (M,), dev, "adapter")
     _packed_ready(packed, ("wq", "s_u8", "a_u8", "sw"), 1, dev, "packed")
-    with _Launch(dev, stream) as st:
+    with _context(dev, stream):
         if out is None:
             out = torch.empty((M, N), dtype=torch.float16, device=dev)
         _ready(out, torch.float16, (M, N), dev, "out")
@@ -664,5 +659,6 @@ def gemm_lora(X, packed, lora, adapter, out=None, workspace=None, stream=None):
         _check(lib.w4a8_gemm_lora(_ptr(X), it, _ptr(packed["wq"]), _ptr(packed["s_u8"]),
                                   _ptr(packed["a_u8"]), _ptr(packed["sw"]), _ptr(A), _ptr(B),
                                   _ptr(lora["scale"]), n, R, _ptr(adapter), _ptr(out), M, N, K,
-                                  packed["group"], _ptr(ws), ws_bytes, st), "w4a8_gemm_lora")
+                                  packed["group"], _ptr(ws), ws_bytes,
+                              _stream()), "w4a8_gemm_lora")
     return out

@@ -52,17 +52,22 @@ struct Choice {
     float w;
 };
 
-// One token per wave, up to 64 VPL experts: lane l holds experts 64 i + l.
+// Keys of one token per wave, up to 64 VPL experts: lane l holds experts
+// 64 i + l.
 template <int IN, int VPL>
-__device__ __forceinline__ Choice choose_wave(const void* logits, size_t t, int E, int k,
-                                              bool renorm) {
+__device__ __forceinline__ void load_keys(const void* logits, size_t t, size_t T, int E,
+                                          unsigned (&key)[VPL]) {
     const int lane = threadIdx.x & 63;
-    unsigned key[VPL];
 #pragma unroll
     for (int i = 0; i < VPL; ++i) {
         const int e = 64 * i + lane;
-        key[i] = e < E ? logit_key(load_logit<IN>(logits, t * E + e)) : 0u;
+        key[i] = t < T && e < E ? logit_key(load_logit<IN>(logits, t * E + e)) : 0u;
     }
+}
+
+template <int VPL>
+__device__ __forceinline__ Choice choose_wave(unsigned (&key)[VPL], int k, bool renorm) {
+    const int lane = threadIdx.x & 63;
     unsigned all = key[0];
 #pragma unroll
     for (int i = 1; i < VPL; ++i) all = MaxU32{}(all, key[i]);
@@ -76,6 +81,7 @@ __device__ __forceinline__ Choice choose_wave(const void* logits, size_t t, int 
         sum = wave_sum(sum);
     }
     Choice c{-1, 0.0f};
+    unsigned mine = 0;  // key of the lane's choice
     for (int j = 0; j < k && best != 0; ++j) {
         int id = -1;
 #pragma unroll
@@ -83,7 +89,10 @@ __device__ __forceinline__ Choice choose_wave(const void* logits, size_t t, int 
             const uint64_t m = __ballot(key[i] == best);
             if (id < 0 && m) id = 64 * i + __builtin_ctzll(m);
         }
-        if (lane == j) c = Choice{id, gate_exp(key_logit(best), top)};
+        if (lane == j) {
+            c.id = id;
+            mine = best;
+        }
         all = 0;
 #pragma unroll
         for (int i = 0; i < VPL; ++i) {
@@ -92,31 +101,33 @@ __device__ __forceinline__ Choice choose_wave(const void* logits, size_t t, int 
         }
         best = wave_reduce(all, MaxU32{});
     }
+    c.w = mine ? gate_exp(key_logit(mine), top) : 0.0f;
     if (renorm) sum = wave_sum(c.w);
     c.w = c.id >= 0 ? __fdiv_rn(c.w, sum) : 0.0f;
     return c;
 }
 
 // Four tokens per wave, up to 16 experts: the 16 lanes of a row hold a
-// token's experts (t0: the wave's first token).
-template <int IN>
-__device__ __forceinline__ Choice choose_row(const void* logits, size_t t0, size_t T, int E, int k,
-                                             bool renorm) {
+// token's experts.
+__device__ __forceinline__ Choice choose_row(unsigned key, int k, bool renorm) {
     const int lane = threadIdx.x & 63, e = lane & 15, row = lane >> 4;
-    const size_t t = t0 + row;
-    unsigned key = (t < T && e < E) ? logit_key(load_logit<IN>(logits, t * E + e)) : 0u;
     unsigned best = row16_reduce(key, MaxU32{});
     const float top = key_logit(best);
     float sum = 0.0f;
     if (!renorm) sum = row16_sum(key ? gate_exp(key_logit(key), top) : 0.0f);
     Choice c{-1, 0.0f};
+    unsigned mine = 0;  // key of the lane's choice
     for (int j = 0; j < k; ++j) {
         const unsigned m = (unsigned)(__ballot(key == best) >> (16 * row)) & 0xFFFFu;
         const int id = best ? __builtin_ctz(m) : -1;  // best is some lane's key, so m != 0
-        if (e == j) c = Choice{id, id >= 0 ? gate_exp(key_logit(best), top) : 0.0f};
+        if (e == j) {
+            c.id = id;
+            mine = best;
+        }
         if (e == id) key = 0u;
         best = row16_reduce(key, MaxU32{});
     }
+    c.w = mine ? gate_exp(key_logit(mine), top) : 0.0f;
     if (renorm) sum = row16_sum(c.w);
     c.w = c.id >= 0 ? __fdiv_rn(c.w, sum) : 0.0f;
     return c;
@@ -129,22 +140,33 @@ __device__ __forceinline__ void choose_tokens(const void* logits, size_t lo, siz
                                               int k, bool renorm, int* ids, float* weights,
                                               Seen seen) {
     constexpr int PW = VPL == 0 ? 4 : 1;  // tokens per wave
+    constexpr int AHEAD = 4;              // steps whose logits are loaded together
+    constexpr int KEYS = VPL == 0 ? 1 : VPL;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    for (size_t t0 = lo + PW * wave; t0 < hi; t0 += PW * kGroupWaves) {
-        Choice c;
-        int j = lane;
-        size_t t = t0;
-        if constexpr (VPL == 0) {
-            c = choose_row<IN>(logits, t0, hi, E, k, renorm);
-            j = lane & 15;
-            t = t0 + (lane >> 4);
-        } else {
-            c = choose_wave<IN, VPL>(logits, t0, E, k, renorm);
+    const int j = VPL == 0 ? lane & 15 : lane, row = VPL == 0 ? lane >> 4 : 0;
+    constexpr size_t STEP = PW * kGroupWaves;
+    for (size_t t0 = lo + PW * wave; t0 < hi; t0 += AHEAD * STEP) {
+        unsigned key[AHEAD][KEYS];
+#pragma unroll
+        for (int i = 0; i < AHEAD; ++i) {
+            const size_t t = t0 + i * STEP + row;
+            if constexpr (VPL == 0)
+                key[i][0] = t < hi && j < E ? logit_key(load_logit<IN>(logits, t * E + j)) : 0u;
+            else
+                load_keys<IN>(logits, t, hi, E, key[i]);
         }
-        if (t < hi && j < k) {
-            ids[t * k + j] = c.id;
-            weights[t * k + j] = c.w;
-            seen((int)(t - lo) * k + j, c.id);
+#pragma unroll
+        for (int i = 0; i < AHEAD; ++i) {
+            if (t0 + i * STEP >= hi) break;
+            Choice c;
+            if constexpr (VPL == 0) c = choose_row(key[i][0], k, renorm);
+            else c = choose_wave(key[i], k, renorm);
+            const size_t t = t0 + i * STEP + row;
+            if (t < hi && j < k) {
+                ids[t * k + j] = c.id;
+                weights[t * k + j] = c.w;
+                seen((int)(t - lo) * k + j, c.id);
+            }
         }
     }
 }
@@ -224,15 +246,29 @@ __global__ __launch_bounds__(kThreads) void route_place_kernel(
     const int S = (int)(min(lo + tb, (size_t)T) - lo) * k;
     const int* bid = ids + lo * k;
     for (int i = threadIdx.x; i < kGroupWaves * E; i += kThreads) hist[i] = 0;
-    int before = 0;  // of expert threadIdx.x, in earlier blocks
-    if ((int)threadIdx.x < E) {
-        int all = 0;
-        for (int b = 0; b < (int)gridDim.x; ++b) {
-            const int c = counts[(size_t)b * E + threadIdx.x];
-            before += b < (int)blockIdx.x ? c : 0;
-            all += c;
+    // totals, and the slots of earlier blocks: part-th of the blocks per group
+    // of E threads, joined by integer adds in LDS
+    int* before = start + E + 1;
+    for (int e = threadIdx.x; e < E; e += kThreads) cnt[e] = before[e] = 0;
+    __syncthreads();
+    const int parts = kThreads / E, part = threadIdx.x / E, pe = threadIdx.x % E;
+    if (part < parts) {
+        int all = 0, mine = 0;
+        for (int b = part; b < (int)gridDim.x; b += 8 * parts) {
+            int c[8];
+#pragma unroll
+            for (int u = 0; u < 8; ++u) {
+                const int bu = b + u * parts;
+                c[u] = bu < (int)gridDim.x ? counts[(size_t)bu * E + pe] : 0;
+            }
+#pragma unroll
+            for (int u = 0; u < 8; ++u) {
+                all += c[u];
+                mine += b + u * parts < (int)blockIdx.x ? c[u] : 0;
+            }
         }
-        cnt[threadIdx.x] = all;
+        atomicAdd(&cnt[pe], all);
+        atomicAdd(&before[pe], mine);
     }
     __syncthreads();
     expert_scan(cnt, start, E);
@@ -240,7 +276,7 @@ __global__ __launch_bounds__(kThreads) void route_place_kernel(
     group_count(hist, S, E, get);
     __syncthreads();
     if ((int)threadIdx.x < E) {
-        int p = start[threadIdx.x] + before;
+        int p = start[threadIdx.x] + before[threadIdx.x];
         for (int w = 0; w < kGroupWaves; ++w) {
             const int c = hist[w * E + threadIdx.x];
             hist[w * E + threadIdx.x] = p;
@@ -264,7 +300,7 @@ template <int IN, int VPL>
 hipError_t route_run(const void* logits, int T, int E, int k, int renorm, int* ids,
                      float* weights, int* offsets, int* rows, const RoutePlan& plan, int* counts,
                      hipStream_t st) {
-    const size_t group_lds = ((size_t)kGroupWaves * E + 2 * E + 1) * sizeof(int);
+    const size_t group_lds = ((size_t)kGroupWaves * E + 3 * E + 1) * sizeof(int);
     if (plan.blocks == 1) {
         hipLaunchKernelGGL((route_small_kernel<IN, VPL>), dim3(1), dim3(kThreads),
                            group_lds + (size_t)T * k * sizeof(int), st, logits, T, E, k, renorm,
@@ -297,18 +333,20 @@ hipError_t route_type(const void* logits, int T, int E, int k, int renorm, int* 
 
 }  // namespace
 
-// One workgroup while its slots fit 16 KiB of LDS and every wave sees few
-// tokens; else blocks of at least 64 tokens, at most 256 blocks.
+// One workgroup while every wave makes one step (its 16 waves share a CU: at
+// four steps each, 61 tokens of 128 experts took 16 us against 8 in two
+// launches over many CUs); else blocks of at least 32 tokens (16 for small
+// calls), at most 512 blocks.
 RoutePlan plan_route(int T, int E, int k) {
     RoutePlan p;
     const int per_pass = kGroupWaves * (E <= 16 ? 4 : 1);
-    if (T <= 4 * per_pass && (long long)T * k <= 4096) {
+    if (T <= per_pass) {
         p.blocks = 1;
         p.tokens = T;
         p.workspace = 0;
         return p;
     }
-    p.tokens = 64 * ((T + 64 * 256 - 1) / (64 * 256));
+    p.tokens = T <= 2048 ? 16 : 32 * (int)((T + 32LL * 512 - 1) / (32 * 512));
     p.blocks = (T + p.tokens - 1) / p.tokens;
     p.workspace = (size_t)p.blocks * E * sizeof(int);
     return p;
