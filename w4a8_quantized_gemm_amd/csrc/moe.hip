@@ -390,14 +390,12 @@ __global__ __launch_bounds__(256) void moe_combine_kernel(const float* __restric
 }
 
 // ---------------------------------------------------------------------------
-// The layer for at most 16 slots, in two launches: every workgroup of the
-// first finds its expert's slots among the ids and quantises their tokens
-// itself, every workgroup of the second quantises h and joins the slots of
-// its 16 channels.  The quantised rows lie in LDS (row stride K + 16 bytes),
-// the first weights are in flight while they are formed.
+// Few slots: every workgroup finds its expert's slots among the ids and
+// quantises their rows itself, into LDS (row stride K + 16 bytes), while the
+// first weights are in flight.  That saves the launches that prepare the
+// rows: one token takes two launches, a few tokens three.
 // ---------------------------------------------------------------------------
-constexpr int kFewSlots = 16;   // of the two-launch layer
-constexpr int kMaskSlots = 64;  // of the kernels that find their slots by ballots
+constexpr int kMaskSlots = 64;  // slots that one wave's ballots can find
 
 // The slots of lane-wise ids (lane = slot): one bit per expert's first slot.
 struct FewSlots {
@@ -460,13 +458,14 @@ __device__ __forceinline__ float quant_row_lds(bool on, const void* row, int K, 
 // channels of each half, the rows quantised by the workgroup itself:
 // HALVES = 2: gate and up of the slots' tokens (rows of X), into h[slot][N / 2];
 // HALVES = 1: down of the slots (rows of h), times the slot's weight, into
-// part[slot][N].  16 rows at a time.
+// part[slot][N].  `cap` rows at a time (more slots of an expert repeat its
+// stream).
 template <int HALVES, int IN, int GROUP>
 __global__ __launch_bounds__(256, 4) void moe_few_kernel(
     const void* __restrict__ X, const int* __restrict__ ids, const float* __restrict__ weights,
     const uint8_t* __restrict__ wq, const uint8_t* __restrict__ s_u8,
     const uint8_t* __restrict__ a_u8, const float* __restrict__ sw, float* __restrict__ out, int S,
-    int E, int k, int N, int K) {
+    int E, int k, int N, int K, int cap) {
     constexpr int NT = 2, TT = HALVES * NT, D = HALVES == 2 ? 2 : 4, WAVES = 4;
     extern __shared__ __attribute__((aligned(16))) uint8_t few_lds[];
     uint8_t* const lds = few_lds;
@@ -511,8 +510,8 @@ __global__ __launch_bounds__(256, 4) void moe_few_kernel(
             st.a[hf] = buf_load4(a_rsrc, pvoff, po);
         }
     };
-    while (mine) {  // the next 16 slots
-    const int count = min(16, __builtin_popcountll(mine));
+    while (mine) {  // the next slots, at most cap (<= 16)
+    const int count = min(cap, __builtin_popcountll(mine));
     Stage st[D];
 #pragma unroll
     for (int d = 0; d < D; ++d)
@@ -607,25 +606,26 @@ __global__ __launch_bounds__(256, 4) void moe_few_kernel(
     }
 }
 
-// Down product of every slot for 16 channels, and their weighted sums: the
-// 16 waves stream the chosen experts' tiles one after the other (a wave's
-// K-tiles of all experts are one sequence, so the pipeline does not drain
-// between them).  P (a power of two, at least S) rows are quantised at once.
+// One token: the down products of its k slots for 16 channels and their
+// weighted sum.  The 16 waves stream the chosen experts' tiles one after the
+// other (a wave's K-tiles of all experts are one sequence, so the pipeline
+// does not drain between them).  P (a power of two, at least k) rows are
+// quantised at once.
 template <int OUT, int GROUP>
 __global__ __launch_bounds__(1024) void moe_few_down_kernel(
     const float* __restrict__ h, const int* __restrict__ ids, const float* __restrict__ weights,
     const uint8_t* __restrict__ wq, const uint8_t* __restrict__ s_u8,
-    const uint8_t* __restrict__ a_u8, const float* __restrict__ sw, void* __restrict__ Y, int T,
-    int E, int k, int H, int K, int P) {
+    const uint8_t* __restrict__ a_u8, const float* __restrict__ sw, void* __restrict__ Y, int E,
+    int S, int H, int K, int P) {
     constexpr int D = 4, WAVES = 16;
     extern __shared__ __attribute__((aligned(16))) uint8_t few_lds[];
     uint8_t* const lds = few_lds;
-    __shared__ float scales[kFewSlots];
+    __shared__ float scales[kMaxTopK];
     __shared__ unsigned part[WAVES];
-    __shared__ float ys[kFewSlots * 16];
+    __shared__ float ys[kMaxTopK * 16];
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int r = lane & 15, G = lane >> 4, S = T * k;
+    const int r = lane & 15, G = lane >> 4;
     const FewSlots f = few_slots(ids, S, E);
     const int KT = K / kTileK, groups = K / GROUP, nt = channel_group();
     const int nk = wave < KT ? (KT - wave + WAVES - 1) / WAVES : 0;
@@ -637,7 +637,7 @@ __global__ __launch_bounds__(1024) void moe_few_down_kernel(
         unsigned s, a;
     };
     // the sequence's next K-tile to load: of expert `in_e`
-    unsigned in_first = (unsigned)f.first;  // at most 16 slots
+    unsigned in_first = (unsigned)f.first;  // k <= 16 slots
     int in_i = 0, in_e = in_first ? __builtin_amdgcn_readlane(f.id, __builtin_ctz(in_first)) : 0;
     auto issue = [&](Stage& st) {
         const int kt = wave + WAVES * in_i;
@@ -755,14 +755,14 @@ __global__ __launch_bounds__(1024) void moe_few_down_kernel(
         ys[tid] = y;
     }
     __syncthreads();
-    if (tid < T * 16) {
-        const int t = tid >> 4, n = nt * kTileN + (tid & 15);
+    if (tid < 16) {
+        const int n = nt * kTileN + tid;
         float y = 0.0f;
-        for (int j = 0; j < k; ++j) y += ys[(t * k + j) * 16 + (tid & 15)];
+        for (int j = 0; j < S; ++j) y += ys[j * 16 + tid];
         if constexpr (OUT == 0)
-            reinterpret_cast<float*>(Y)[(size_t)t * H + n] = y;
+            reinterpret_cast<float*>(Y)[n] = y;
         else
-            reinterpret_cast<unsigned short*>(Y)[(size_t)t * H + n] =
+            reinterpret_cast<unsigned short*>(Y)[n] =
                 OUT == 1 ? f32_to_f16_bits(y) : f32_to_bf16_bits(y);
     }
 }
@@ -771,20 +771,33 @@ size_t moe_workspace(int T, int k, int H, int F) { return MoeLayout(T, k, H, F).
 
 namespace {
 
-// Limits of the kernels that quantise their own rows: LDS that leaves room for
-// two workgroups per CU, and elements per workgroup (every workgroup of an
-// expert repeats the work).
-constexpr size_t kFewLds = 80 * 1024;
-constexpr float kFewElements = 16384.0f;
-
-// Row blocks of 16 that share a decoded weight, from the slots per expert a
-// batch has on average and three of their standard deviations above it (an
-// expert with more rows repeats its stream): 131 tokens, two of 16 experts
-// each (4096 x 6400): 200 us with one block, 163 with two, 172 with four.
-int row_blocks(int T, int S, int E) {
+// Rows that few experts exceed: the slots per expert a batch has on average
+// and three of their standard deviations, or a row per token.
+float most_rows(int T, int S, int E) {
     const float avg = (float)S / (float)E;
-    const float most = fminf(avg + 3.0f * sqrtf(avg), (float)T);
-    return most <= 16.0f ? 1 : most <= 32.0f ? 2 : 4;
+    return fminf(avg + 3.0f * sqrtf(avg), (float)T);
+}
+
+// The kernels that quantise their own rows run while the rows leave room for
+// four workgroups per CU (at 66 KiB, two per CU, 32 tokens over 16 experts of
+// 4096 x 2048 took 77 us against 54 with prepared rows).  Otherwise, in us,
+// prepared rows / rows of their own / one token in two launches:
+//   8 experts 14336 x 4096, top 2:   1 token 48.3 / 46.2 / 42.3, 2: 76.9 / 73.0
+//   64 experts 1408 x 2048, top 6:   1 token 24.8 / 18.5 / 18.3, 2: 26.7 / 22.0,
+//                                    8: 44.1 / 42.2
+//   16 experts 4096 x 2048, top 2:   1 token 23.4 / 17.5 / 16.2, 4: 35.6 / 30.0
+// (the two-launch form lost to three from two tokens on: 22.1 against 21.1).
+constexpr size_t kFewLds = 40 * 1024;
+
+// Row blocks of 16 that share a decoded weight (an expert with more rows
+// repeats its stream).  us with one / two / four blocks:
+//   131 tokens, two of 16 experts 6400 x 4096:   200 / 163 / 172
+//   48 tokens, two of 8 experts 4096 x 2048:     47.8 / 41.6 / 49.3
+//   200 tokens, the same:                        119.9 / 95.1 / 90.1
+//   64 tokens, six of 64 experts 1408 x 2048:    71.9 / 71.9 / 109
+int row_blocks(int T, int S, int E) {
+    const float most = most_rows(T, S, E);
+    return most <= 20.0f ? 1 : most <= 40.0f ? 2 : 4;
 }
 
 // Two tiles of each half per workgroup.  Waves splitting K: four, eight for
@@ -816,39 +829,38 @@ size_t few_rows_lds(int rows, int K) { return 16 + (size_t)rows * (K + 16); }
 
 template <int HALVES, int IN, int GROUP>
 void launch_few_type(const void* X, const int* ids, const float* weights, const MoeWeights& w,
-                     float* out, int S, int E, int k, int N, int K, hipStream_t st) {
+                     float* out, int S, int E, int k, int N, int K, int cap, hipStream_t st) {
     const dim3 grid(N / HALVES / 32, E < S ? E : S);
     const size_t red = (size_t)4 * HALVES * 2 * 256 * sizeof(int);  // the sums, over the rows
-    const size_t lds = few_rows_lds(S < 16 ? S : 16, K);
+    const size_t lds = few_rows_lds(cap, K);
     hipLaunchKernelGGL((moe_few_kernel<HALVES, IN, GROUP>), grid, dim3(256), lds > red ? lds : red,
-                       st, X, ids, weights, w.wq, w.s_u8, w.a_u8, w.sw, out, S, E, k, N, K);
+                       st, X, ids, weights, w.wq, w.s_u8, w.a_u8, w.sw, out, S, E, k, N, K, cap);
 }
 
 template <int GROUP>
 void launch_few_up(const void* X, int in_type, const int* ids, const MoeWeights& w, float* h,
-                   int S, int E, int k, int F, int H, hipStream_t st) {
+                   int S, int E, int k, int F, int H, int cap, hipStream_t st) {
     if (in_type == 1)
-        launch_few_type<2, 1, GROUP>(X, ids, nullptr, w, h, S, E, k, 2 * F, H, st);
+        launch_few_type<2, 1, GROUP>(X, ids, nullptr, w, h, S, E, k, 2 * F, H, cap, st);
     else if (in_type == 2)
-        launch_few_type<2, 2, GROUP>(X, ids, nullptr, w, h, S, E, k, 2 * F, H, st);
+        launch_few_type<2, 2, GROUP>(X, ids, nullptr, w, h, S, E, k, 2 * F, H, cap, st);
     else
-        launch_few_type<2, 0, GROUP>(X, ids, nullptr, w, h, S, E, k, 2 * F, H, st);
+        launch_few_type<2, 0, GROUP>(X, ids, nullptr, w, h, S, E, k, 2 * F, H, cap, st);
 }
 
-size_t few_down_lds(int S, int F) {
-    return few_rows_lds(S, F) + (size_t)16 * S * 16 * sizeof(int);
+size_t few_down_lds(int k, int F) {
+    return few_rows_lds(k, F) + (size_t)16 * k * 16 * sizeof(int);
 }
 
 template <int GROUP>
-void launch_few_down(const float* h, const int* ids, const float* weights, int T, int E, int k,
+void launch_few_down(const float* h, const int* ids, const float* weights, int E, int k,
                      const MoeWeights& w, void* Y, int out_type, int H, int F, hipStream_t st) {
-    const int S = T * k;
     int P = 1;
-    while (P < S) P *= 2;
+    while (P < k) P *= 2;
 #define FEW_DOWN(O)                                                                            \
     hipLaunchKernelGGL((moe_few_down_kernel<O, GROUP>), dim3(H / kTileN), dim3(1024),          \
-                       few_down_lds(S, F), st, h, ids, weights, w.wq, w.s_u8, w.a_u8, w.sw, Y, \
-                       T, E, k, H, F, P)
+                       few_down_lds(k, F), st, h, ids, weights, w.wq, w.s_u8, w.a_u8, w.sw, Y, \
+                       E, k, H, F, P)
     if (out_type == 1) FEW_DOWN(1);
     else if (out_type == 2) FEW_DOWN(2);
     else FEW_DOWN(0);
@@ -882,24 +894,25 @@ hipError_t launch_moe(const void* X, int in_type, const int* ids, const float* w
     float* sh = reinterpret_cast<float*>(ws + lay.sh);
     float* part = reinterpret_cast<float*>(ws + lay.part);
     const int S = T * k, experts = E < S ? E : S;
-    const float rows = S > E ? (float)S / (float)E : 1.0f;  // per chosen expert
-    const bool up = S <= kMaskSlots && few_rows_lds(S < 16 ? S : 16, H) <= kFewLds &&
-                    rows * H <= kFewElements;
-    const bool down = S <= kMaskSlots && few_rows_lds(S < 16 ? S : 16, F) <= kFewLds &&
-                      rows * F <= kFewElements;
-    const bool join = S <= kFewSlots && few_down_lds(S, F) <= 144 * 1024;
+    // rows of an expert that one stream has to serve, a power of two; the
+    // kernels that quantise their own rows take those and their elements
+    int cap = 1;
+    while (cap < 16 && (float)cap < most_rows(T, S, E)) cap *= 2;
+    const bool up = S <= kMaskSlots && few_rows_lds(cap, H) <= kFewLds;
+    const bool join = T == 1 && few_down_lds(k, F) <= 144 * 1024;
+    const bool down = S <= kMaskSlots && few_rows_lds(cap, F) <= kFewLds;
     if (up && (join || down)) {
-        if (group == 64) launch_few_up<64>(X, in_type, ids, w13, h, S, E, k, F, H, st);
-        else launch_few_up<128>(X, in_type, ids, w13, h, S, E, k, F, H, st);
+        if (group == 64) launch_few_up<64>(X, in_type, ids, w13, h, S, E, k, F, H, cap, st);
+        else launch_few_up<128>(X, in_type, ids, w13, h, S, E, k, F, H, cap, st);
         if (join) {
-            if (group == 64)
-                launch_few_down<64>(h, ids, weights, T, E, k, w2, Y, out_type, H, F, st);
-            else
-                launch_few_down<128>(h, ids, weights, T, E, k, w2, Y, out_type, H, F, st);
+            if (group == 64) launch_few_down<64>(h, ids, weights, E, k, w2, Y, out_type, H, F, st);
+            else launch_few_down<128>(h, ids, weights, E, k, w2, Y, out_type, H, F, st);
             return hipGetLastError();
         }
-        if (group == 64) launch_few_type<1, 0, 64>(h, ids, weights, w2, part, S, E, k, H, F, st);
-        else launch_few_type<1, 0, 128>(h, ids, weights, w2, part, S, E, k, H, F, st);
+        if (group == 64)
+            launch_few_type<1, 0, 64>(h, ids, weights, w2, part, S, E, k, H, F, cap, st);
+        else
+            launch_few_type<1, 0, 128>(h, ids, weights, w2, part, S, E, k, H, F, cap, st);
         launch_combine(part, ids, T, E, k, H, Y, out_type, st);
         return hipGetLastError();
     }
