@@ -465,13 +465,24 @@ def gemm_w8a8(Xq, sx, packed, out_type: int = OUT_F16, splitk: int = 0, out=None
 # is; every tensor must live there.  Outputs and workspaces that are not given
 # are allocated on the stream the call runs on.
 
+try:  # the current stream of a device as an integer, without a Stream object
+    from torch._C import _cuda_getCurrentRawStream as _raw_stream
+except ImportError:
+    def _raw_stream(index):
+        return torch.cuda.current_stream(index).cuda_stream
+
+
 def _ready(t, dtype, shape, device, name):
     """A contiguous tensor of this type and shape (a tuple) on this device.
     These calls take microseconds on the GPU, so the check is one expression
     and the reason is looked for only when it fails."""
-    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape
-            and t.device == device and t.is_contiguous()):
-        _not_ready(t, dtype, shape, device, name)
+    try:
+        if (t.dtype is dtype and t.shape == shape and t.get_device() == device.index
+                and t.is_contiguous()):
+            return
+    except AttributeError:
+        pass
+    _not_ready(t, dtype, shape, device, name)
 
 
 def _not_ready(t, dtype, shape, device, name):
@@ -521,15 +532,20 @@ def _context(device, stream):
     return _HERE
 
 
-def _workspace(workspace, need, device):
-    """(tensor, bytes) of the caller's workspace, or a new one."""
+def _workspace(workspace, size, dims, device):
+    """(tensor, address, bytes) of the caller's workspace, whose size the
+    library checks, or of a new one of size(*dims) bytes."""
     if workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=device) if need else None
-    elif workspace.device != device:
+        need = size(*dims)
+        if not need:
+            return None, None, 0
+        workspace = torch.empty(need, dtype=torch.uint8, device=device)
+        return workspace, workspace.data_ptr(), need
+    if workspace.device != device:
         raise ValueError(f"workspace must be on {device}, got {workspace.device}")
-    elif not workspace.is_contiguous():
+    if not workspace.is_contiguous():
         raise ValueError("workspace must be contiguous")
-    return workspace, 0 if workspace is None else workspace.numel() * workspace.element_size()
+    return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 
 def _packed_ready(p, keys, E, device, name):
@@ -571,11 +587,11 @@ def route(logits, k: int, renormalize: bool = True, out=None, workspace=None, st
             _ready(out["weights"], torch.float32, (T, k), dev, "out['weights']")
             _ready(out["offsets"], torch.int32, (E + 1,), dev, "out['offsets']")
             _ready(out["rows"], torch.int32, (T * k,), dev, "out['rows']")
-        ws, ws_bytes = _workspace(workspace, route_workspace_size(T, E, k), dev)
-        _check(lib.w4a8_route(_ptr(logits), it, T, E, k, int(bool(renormalize)),
-                              _ptr(out["ids"]), _ptr(out["weights"]), _ptr(out["offsets"]),
-                              _ptr(out["rows"]), _ptr(ws), ws_bytes,
-                              _stream()), "w4a8_route")
+        ws, ws_ptr, ws_bytes = _workspace(workspace, route_workspace_size, (T, E, k), dev)
+        _check(lib.w4a8_route(logits.data_ptr(), it, T, E, k, 1 if renormalize else 0,
+                              out["ids"].data_ptr(), out["weights"].data_ptr(),
+                              out["offsets"].data_ptr(), out["rows"].data_ptr(), ws_ptr, ws_bytes,
+                              _raw_stream(dev.index)), "w4a8_route")
     return out
 
 
@@ -614,12 +630,12 @@ def moe(X, ids, weights, w13, w2, out=None, workspace=None, stream=None):
             out = torch.empty((T, H), dtype=X.dtype, device=dev)
         ot = _float_type(out, "out")
         _ready(out, out.dtype, (T, H), dev, "out")
-        ws, ws_bytes = _workspace(workspace, moe_workspace_size(T, E, k, H, F), dev)
-        _check(lib.w4a8_moe(_ptr(X), it, _ptr(ids), _ptr(weights), T, E, k, _ptr(w13["wq"]),
-                            _ptr(w13["s_u8"]), _ptr(w13["a_u8"]), _ptr(w13["sw"]),
-                            _ptr(w2["wq"]), _ptr(w2["s_u8"]), _ptr(w2["a_u8"]), _ptr(w2["sw"]),
-                            _ptr(out), ot, H, F, g, _ptr(ws), ws_bytes,
-                              _stream()), "w4a8_moe")
+        ws, ws_ptr, ws_bytes = _workspace(workspace, moe_workspace_size, (T, E, k, H, F), dev)
+        _check(lib.w4a8_moe(X.data_ptr(), it, ids.data_ptr(), weights.data_ptr(), T, E, k,
+                            w13["wq"].data_ptr(), w13["s_u8"].data_ptr(), w13["a_u8"].data_ptr(),
+                            w13["sw"].data_ptr(), w2["wq"].data_ptr(), w2["s_u8"].data_ptr(),
+                            w2["a_u8"].data_ptr(), w2["sw"].data_ptr(), out.data_ptr(), ot, H, F,
+                            g, ws_ptr, ws_bytes, _raw_stream(dev.index)), "w4a8_moe")
     return out
 
 
@@ -655,10 +671,11 @@ def gemm_lora(X, packed, lora, adapter, out=None, workspace=None, stream=None):
         if out is None:
             out = torch.empty((M, N), dtype=torch.float16, device=dev)
         _ready(out, torch.float16, (M, N), dev, "out")
-        ws, ws_bytes = _workspace(workspace, gemm_lora_workspace_size(M, N, K, R), dev)
-        _check(lib.w4a8_gemm_lora(_ptr(X), it, _ptr(packed["wq"]), _ptr(packed["s_u8"]),
-                                  _ptr(packed["a_u8"]), _ptr(packed["sw"]), _ptr(A), _ptr(B),
-                                  _ptr(lora["scale"]), n, R, _ptr(adapter), _ptr(out), M, N, K,
-                                  packed["group"], _ptr(ws), ws_bytes,
-                              _stream()), "w4a8_gemm_lora")
+        ws, ws_ptr, ws_bytes = _workspace(workspace, gemm_lora_workspace_size, (M, N, K, R), dev)
+        _check(lib.w4a8_gemm_lora(X.data_ptr(), it, packed["wq"].data_ptr(),
+                                  packed["s_u8"].data_ptr(), packed["a_u8"].data_ptr(),
+                                  packed["sw"].data_ptr(), A.data_ptr(), B.data_ptr(),
+                                  lora["scale"].data_ptr(), n, R, adapter.data_ptr(),
+                                  out.data_ptr(), M, N, K, packed["group"], ws_ptr, ws_bytes,
+                                  _raw_stream(dev.index)), "w4a8_gemm_lora")
     return out
