@@ -158,113 +158,157 @@ __device__ __forceinline__ void mfma16_drain(v4i (&acc)[RB][4]) {
 
 }  // namespace
 
+// LDS of a workgroup whose epilogue adds low-rank adapters: per row its
+// adapter (-1: none), scale and operands of the first 32 ranks (8 pieces of
+// 16 bytes, high and low parts of each 8 ranks, and one piece of padding),
+// per channel its scale.
+constexpr unsigned kLoraVStride = 8 * 16 + 16;
+template <int MT, int LORA>
+struct LoraLds {
+    uint8_t v[MT * kLoraVStride];
+    float backs[LORA == 1 ? MT * 4 : 4];  // [32 ranks][row]
+    float sx[MT], sw[kNT];
+    int ids[MT];
+};
+
+// V operands of the s0-th to (s1 - 1)-th 32 ranks of the workgroup's rows:
+// four threads split a row's 32 ranks, once for all waves.
+template <int MT, int LORA>
+__device__ __forceinline__ void lora_stage_v(const LoraArgs& lora, int m0, int row_hi, int s0,
+                                             int s1, uint8_t* dst, float* backs) {
+    for (int i = threadIdx.x; i < MT * 4 * (s1 - s0); i += 256) {
+        const int row = (i >> 2) % MT, s = s0 + (i >> 2) / MT, k0 = 32 * s + 8 * (i & 3);
+        float v[8] = {};
+        if (m0 + row < row_hi && k0 < lora.R) {  // (rows without an adapter are not used)
+            const v4f* p = reinterpret_cast<const v4f*>(lora.V + (size_t)(m0 + row) * lora.R + k0);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[j] = p[j >> 2][j & 3];
+        }
+        const LoraV o = lora_split<LORA, 1, 2>(v);
+        v4i* d = reinterpret_cast<v4i*>(dst + (unsigned)((s - s0) * MT + row) * kLoraVStride);
+        d[2 * (i & 3)] = o.hi;
+        d[2 * (i & 3) + 1] = o.lo;
+        if (LORA == 1 && (i & 3) == 0) backs[s * MT + row] = o.back;
+    }
+}
+
+// Accumulators of row blocks rb .. rb + PB - 1 (uniform), by a tree of
+// branches.  Read in assembly, so that the copies stay where they are:
+// hoisted out of the epilogue's loop they would need a register per
+// accumulator, and the allocator, spilling parts of accumulators, has lost
+// one.
+template <int LO, int HI, int PB, int RB>
+__device__ __forceinline__ void read_blocks(const v4i (&acc)[RB][4], int rb, v4i (&cur)[PB][4]) {
+    if constexpr (HI - LO == PB) {
+#pragma unroll
+        for (int p = 0; p < PB; ++p)
+#pragma unroll
+            for (int cb = 0; cb < 4; ++cb)
+#pragma unroll
+                for (int v = 0; v < 4; ++v) {
+                    int x;
+                    asm volatile("v_accvgpr_read_b32 %0, %1" : "=v"(x) : "a"(acc[LO + p][cb][v]));
+                    cur[p][cb][v] = x;
+                }
+    } else {
+        constexpr int MID = (LO + HI) / 2;
+        if (rb < MID) read_blocks<LO, MID>(acc, rb, cur);
+        else read_blocks<MID, HI>(acc, rb, cur);
+    }
+}
+
 // Epilogue with low-rank adapters.  Accumulator layout as in the kernel's own
 // epilogue.  Row blocks are walked in a loop that is not unrolled, with a
 // uniform choice of the block's accumulators in front (their registers have
 // constant numbers): sixteen copies of the adapters' code would stream
 // through the instruction cache for every tile (4096 x 28672 x 8192, rank 16:
-// 864 us with the copies).  The rows' V, ids and scales lie in LDS where they
-// fit beside the staging block (ranks up to 72 or more).
+// 864 us with the copies; two blocks a step 769, one 787, the projection alone
+// 699 on one box).
 template <int MT, int LORA>
 __device__ __forceinline__ void mfma16_lora_epilogue(v4i (&acc)[MT / 16][4], uint8_t* lds,
-                                                     unsigned lds_bytes, float* sxs,
-                                                     const float* sw, const LoraArgs& lora, unsigned short* Y,
+                                                     unsigned lds_bytes,
+                                                     LoraLds<MT, LORA>& pre,
+                                                     const LoraArgs& lora, unsigned short* Y,
                                                      int m0, int n0, int row_hi, int N) {
-    constexpr int RSTR = 64 * 2 + 16;  // padded row stride of the fp16 staging block
-    // LDS behind the staging blocks: per row and 32 ranks, 8 pieces of 16
-    // bytes (high and low operand parts of each 8 ranks), padded by one
-    constexpr unsigned VOFF = kWaves * 16 * RSTR;
-    constexpr unsigned VSTR = 8 * 16 + 16;
-    __shared__ int ids[MT];
-    __shared__ float backs[LORA == 1 ? MT * 4 : 1];                // [32 ranks][row]
-    __shared__ __attribute__((aligned(16))) float sws[kNT];  // the workgroup's channel scales
+    constexpr int PB = MT == 256 ? 2 : 1;  // row blocks per step (128-row tiles: registers for one)
+    constexpr int RSTR = 64 * 2 + 16;      // padded row stride of the fp16 staging block
+    constexpr unsigned VOFF = kWaves * 16 * PB * RSTR;
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const int r = lane & 15, G = lane >> 4;
-    sws[tid] = sw[n0 - wave * kColsPerWave + tid];
+    // ranks past the first 32: behind the staging blocks where they fit
     const int ns = (lora.R + 31) / 32;
-    const bool v_in_lds = VOFF + (unsigned)(MT * ns) * VSTR <= lds_bytes;
-    ids[tid % MT] = lora_id(lora, m0 + tid % MT, m0 + tid % MT < row_hi);
-    if (v_in_lds) {  // four threads split a row's 32 ranks once for all waves
-        for (int i = tid; i < MT * 4 * ns; i += 256) {
-            const int row = (i >> 2) % MT, s = (i >> 2) / MT, k0 = 32 * s + 8 * (i & 3);
-            float v[8] = {};
-            if (m0 + row < row_hi && k0 < lora.R) {  // (rows without an adapter are not used)
-                const v4f* p = reinterpret_cast<const v4f*>(lora.V + (size_t)(m0 + row) * lora.R + k0);
-#pragma unroll
-                for (int j = 0; j < 8; ++j) v[j] = p[j >> 2][j & 3];
-            }
-            const LoraV o = lora_split<LORA, 1, 2>(v);
-            v4i* dst = reinterpret_cast<v4i*>(lds + VOFF + (unsigned)(s * MT + row) * VSTR);
-            dst[2 * (i & 3)] = o.hi;
-            dst[2 * (i & 3) + 1] = o.lo;
-            if (LORA == 1 && (i & 3) == 0) backs[s * MT + row] = o.back;
-        }
+    const bool v_in_lds = VOFF + (unsigned)(MT * (ns - 1)) * kLoraVStride <= lds_bytes;
+    if (v_in_lds && ns > 1) {
+        lora_stage_v<MT, LORA>(lora, m0, row_hi, 1, ns, lds + VOFF, pre.backs);
+        __syncthreads();
     }
-    __syncthreads();
-    uint8_t* stage = lds + wave * (16 * RSTR);
+    uint8_t* stage = lds + wave * (16 * PB * RSTR);
+    unsigned short* yp = Y + (size_t)(m0 + (lane >> 3)) * N + n0 + (lane & 7) * 8;
     LoraHeld<MT == 256 ? 4 : 1> held;
 #pragma clang loop unroll(disable)
-    for (int rb = 0; rb < MT / 16; ++rb) {
-        // Read in assembly, so that the copies stay where they are: hoisted out
-        // of the loop they would need a register per accumulator, and the
-        // allocator, spilling parts of accumulators, has lost one.
-        v4i cur[4];
-        static_for<MT / 16>([&](auto i) {
-            if (rb == decltype(i)::value) {
+    for (int rb = 0; rb < MT / 16; rb += PB) {
+        v4i cur[PB][4];
+        read_blocks<0, MT / 16, PB>(acc, rb, cur);
+        int id[PB];
+        float sm[PB];
+        v4f y[PB][4];
 #pragma unroll
-                for (int cb = 0; cb < 4; ++cb)
-#pragma unroll
-                    for (int v = 0; v < 4; ++v) {
-                        int x;
-                        asm volatile("v_accvgpr_read_b32 %0, %1"
-                                     : "=v"(x)
-                                     : "a"(acc[decltype(i)::value][cb][v]));
-                        cur[cb][v] = x;
-                    }
-            }
-        });
-        const int row = 16 * rb + r;
-        const int id = ids[row];
-        const float sm = sxs[row];
-        v4f y[4];
+        for (int p = 0; p < PB; ++p) {
+            id[p] = pre.ids[16 * (rb + p) + r];
+            sm[p] = pre.sx[16 * (rb + p) + r];
+        }
 #pragma unroll
         for (int cb = 0; cb < 4; ++cb) {
             const v4f w =
-                *reinterpret_cast<const v4f*>(&sws[wave * kColsPerWave + 16 * cb + 4 * G]);
+                *reinterpret_cast<const v4f*>(&pre.sw[wave * kColsPerWave + 16 * cb + 4 * G]);
 #pragma unroll
-            for (int v = 0; v < 4; ++v) y[cb][v] = ((float)cur[cb][v] * sm) * w[v];
+            for (int p = 0; p < PB; ++p)
+#pragma unroll
+                for (int v = 0; v < 4; ++v) y[p][cb][v] = ((float)cur[p][cb][v] * sm[p]) * w[v];
         }
-        lora_add_held<LORA>(
-            lora, id, N, n0,
-            [&](int s) {
-                if (!v_in_lds) {
-                    float v[8];
-                    lora_load_v(lora, m0 + row, id >= 0, s, v);
-                    return lora_split<LORA>(v);
-                }
-                const v4i* p =
-                    reinterpret_cast<const v4i*>(lds + VOFF + (unsigned)(s * MT + row) * VSTR);
-                return LoraV{p[2 * G], p[2 * G + 1], LORA == 1 ? backs[s * MT + row] : 1.0f};
-            },
-            held, y);
 #pragma unroll
-        for (int cb = 0; cb < 4; ++cb) {
-            unsigned short h[4];
-#pragma unroll
-            for (int v = 0; v < 4; ++v) h[v] = f32_to_f16_bits(y[cb][v]);
-            *reinterpret_cast<uint2*>(stage + r * RSTR + (16 * cb + 4 * G) * 2) =
-                uint2{h[0] | ((unsigned)h[1] << 16), h[2] | ((unsigned)h[3] << 16)};
+        for (int p = 0; p < PB; ++p) {
+            const int row = 16 * (rb + p) + r;
+            lora_add_held<LORA>(
+                lora, id[p], N, n0,
+                [&](int s) {
+                    if (s > 0 && !v_in_lds) {
+                        float v[8];
+                        lora_load_v(lora, m0 + row, id[p] >= 0, s, v);
+                        return lora_split<LORA>(v);
+                    }
+                    const uint8_t* base =
+                        s == 0 ? pre.v : lds + VOFF + (unsigned)((s - 1) * MT) * kLoraVStride;
+                    const v4i* q = reinterpret_cast<const v4i*>(base + (unsigned)row * kLoraVStride);
+                    return LoraV{q[2 * G], q[2 * G + 1],
+                                 LORA == 1 ? pre.backs[s * MT + row] : 1.0f};
+                },
+                held, y[p]);
         }
-        __builtin_amdgcn_s_waitcnt(0xc07f);  // lgkmcnt(0): this wave's LDS writes done
+#pragma unroll
+        for (int p = 0; p < PB; ++p)
+#pragma unroll
+            for (int cb = 0; cb < 4; ++cb) {
+                unsigned short h[4];
+#pragma unroll
+                for (int v = 0; v < 4; ++v) h[v] = f32_to_f16_bits(y[p][cb][v]);
+                *reinterpret_cast<uint2*>(stage + (16 * p + r) * RSTR + (16 * cb + 4 * G) * 2) =
+                    uint2{h[0] | ((unsigned)h[1] << 16), h[2] | ((unsigned)h[3] << 16)};
+            }
+        // LDS operations of one wave complete in order: only the compiler has
+        // to keep these reads behind the writes, and the next block's writes
+        // behind these reads
+        asm volatile("" ::: "memory");
         __builtin_amdgcn_wave_barrier();
+        const int left = row_hi - m0 - 16 * rb - (lane >> 3);  // rows from this lane's on
 #pragma unroll
-        for (int w = 0; w < 2; ++w) {  // 16 rows of eight 16-byte pieces
-            const int q = lane + 64 * w, sr = q >> 3, piece = q & 7;
-            const int m = m0 + 16 * rb + sr;
-            const v4i val = *reinterpret_cast<const v4i*>(stage + sr * RSTR + piece * 16);
-            if (m < row_hi) store16_result<false>(Y + (size_t)m * N + n0 + piece * 8, val);
+        for (int w = 0; w < 2 * PB; ++w) {  // eight rows of eight 16-byte pieces
+            const v4i val = *reinterpret_cast<const v4i*>(stage + (8 * w + (lane >> 3)) * RSTR +
+                                                          (lane & 7) * 16);
+            if (8 * w < left) store16_result<false>(yp + (size_t)(8 * w) * N, val);
         }
-        __builtin_amdgcn_s_waitcnt(0xc07f);
+        yp += (size_t)(16 * PB) * N;
+        asm volatile("" ::: "memory");
         __builtin_amdgcn_wave_barrier();
     }
 }
@@ -298,7 +342,7 @@ __device__ __forceinline__ void mfma16_body(
     constexpr unsigned XB = MT * 128;     // bytes of one X tile
     constexpr unsigned XSTEP = KIN * XB;  // one K-step's X tiles, one per K part
     __shared__ __attribute__((aligned(1024))) uint8_t xs[3 * XSTEP];
-    __shared__ float sxs[MT];
+    __shared__ float sxs[LORA ? 1 : MT];
 
     const int tid = threadIdx.x;
     const int lane = tid & 63;
@@ -417,6 +461,17 @@ __device__ __forceinline__ void mfma16_body(
     for (int pi = 0; pi < kLoads; ++pi) w_load(0, pi, we);
 #pragma unroll
     for (int pi = 0; pi < kLoads; ++pi) w_load(kw1, pi, wo);
+    // what the adapters' epilogue needs is fetched behind the first tiles
+    [[maybe_unused]] __shared__ std::conditional_t<LORA != 0, LoraLds<MT, LORA>, char> pre;
+    if constexpr (LORA != 0) {
+        const bool on = tid < MT && m0 + tid < row_hi;
+        if (tid < MT) {
+            pre.ids[tid] = lora_id(lora, m0 + tid, on);
+            pre.sx[tid] = on ? sx[m0 + tid] : 0.0f;
+        }
+        pre.sw[tid] = sw[tc.tn * kNT + tid];
+        lora_stage_v<MT, LORA>(lora, m0, row_hi, 0, 1, pre.v, pre.backs);
+    }
     if constexpr (W8) {
         static_for<16>([&](auto k) { mov16_step<0, decltype(k)::value>(we, B); });
     } else {
@@ -508,13 +563,13 @@ __device__ __forceinline__ void mfma16_body(
     // padded by 16 bytes so a write touches distinct banks -- and each row is
     // then written to memory as whole 16-byte pieces of one 128-byte segment
     // (final output, or this split's int32 partial).
-    constexpr bool SCALED = (OUT == 0) && !PARTIAL;
-    if (SCALED) sxs[tid % MT] = (m0 + tid % MT < row_hi) ? sx[m0 + tid % MT] : 0.0f;
     if constexpr (LORA != 0) {
-        mfma16_lora_epilogue<MT, LORA>(acc, xs, 3 * XSTEP, sxs, sw, lora,
+        mfma16_lora_epilogue<MT, LORA>(acc, xs, 3 * XSTEP, pre, lora,
                                        reinterpret_cast<unsigned short*>(Y), m0, n0, row_hi, N);
         return;
     }
+    constexpr bool SCALED = (OUT == 0) && !PARTIAL;
+    if (SCALED) sxs[tid % MT] = (m0 + tid % MT < row_hi) ? sx[m0 + tid % MT] : 0.0f;
     float swv[4][4];
 #pragma unroll
     for (int cb = 0; cb < 4; ++cb)
