@@ -401,7 +401,7 @@ w4a8_status_t w8a8_gemm(const int8_t* X, const float* sx, const int8_t* wq8,
  * 1 <= E <= W4A8_MAX_EXPERTS, 1 <= k <= min(E, W4A8_MAX_TOPK), T * E < 2^31.
  * T = 0 writes offsets (zeros) only; the other pointers may be NULL then.
  * ids, weights, offsets, rows: 4-byte aligned.  workspace: at least
- * w4a8_route_workspace_size bytes (0 for a decode batch: NULL allowed),
+ * w4a8_route_workspace_size bytes (0 for a few tokens: NULL allowed),
  * 16-byte aligned.  No atomics order anything: results are reproducible.
  */
 size_t w4a8_route_workspace_size(int T, int E, int k);
@@ -448,8 +448,9 @@ w4a8_status_t w4a8_moe(const void* X, int in_type, const int32_t* ids,
  *   Y[m] = fp16_rne( (acc[m] * sx[m]) * sw
  *                    + scale[a] * (X[m] . A[a]^T) . B[a]^T ),  a = adapter[m]
  * acc as w4a8_gemm on the INT8 rows (Xq, sx) that w4a8_quant_act_ex gives
- * for X; the adapter's products are float32 sums over the stored values (the
- * inner one is kept to at least 16 significant bits), and Y is rounded once.
+ * for X; the adapter's products are float32 sums over the stored values, the
+ * inner one kept as two numbers of in_type (16 significant bits; for fp16
+ * at least 2^-38 of the largest of 32 ranks), and Y is rounded once.
  *   X: [M][K], A: [n_adapters][R][K], B: [n_adapters][N][R], all fp16 or all
  *     bfloat16 (in_type); scale: float32 [n_adapters]; adapter: int32 [M],
  *     values outside [0, n_adapters) select none, in any order.  Adapters of

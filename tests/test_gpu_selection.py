@@ -147,6 +147,16 @@ MOE = [
     (70, 3, 2, 256, 384, 128, "bf16"),
     (130, 2, 2, 384, 256, 64, "f16"),     # 130 rows of each
     (256, 512, 16, 128, 128, 128, "f16"),  # the most experts, choices and tokens
+    # one token in two launches: the most choices, and rows that fill the LDS
+    (1, 512, 16, 256, 256, 64, "bf16"),
+    (1, 16, 8, 128, 16384, 128, "f16"),
+    (1, 16, 9, 128, 16384, 128, "f16"),   # one more does not fit
+    # up to 64 slots, rows quantised by the products' workgroups
+    (2, 8, 2, 4096, 512, 128, "f32"),
+    (8, 8, 8, 128, 256, 64, "f16"),
+    (4, 2, 2, 1024, 8192, 128, "bf16"),
+    (64, 64, 1, 256, 128, 64, "f16"),
+    (65, 64, 1, 256, 128, 64, "f16"),     # 65 slots: prepared rows
 ]
 
 
@@ -197,6 +207,33 @@ def test_moe_odd_ids_and_rows():
     none = torch.full((T, k), -1, dtype=torch.int32, device=DEV)
     w4.moe(X, none, torch.from_numpy(w).to(DEV), w13, w2, out=Y)
     assert (f64(Y) == 0).all()
+
+
+@pytest.mark.parametrize("T,k", [(1, 6), (1, 16), (5, 4), (8, 8), (16, 4)])
+def test_moe_few_slots_odd_ids(T, k):
+    """The forms for few slots: ids outside the experts, an expert many times
+    over (more rows than a stream serves at once), zero and negative weights,
+    tokens that are not finite, calls without any expert."""
+    E, H, F, g = 12, 256, 384, 64
+    rng = np.random.default_rng(40 + T + k)
+    w13, W13, sw13 = experts(E, 2 * F, H, g, 3500)
+    w2, W2, sw2 = experts(E, H, F, g, 4500)
+    cases = [np.full((T, k), 7), rng.integers(-2, E + 2, (T, k)), np.full((T, k), -1),
+             rng.integers(0, 2, (T, k)) * 9, np.where(rng.random((T, k)) < 0.7, 3, 1 << 30)]
+    for i, ids in enumerate(cases):
+        say(f"moe few T={T} k={k} ids {i}")
+        ids = ids.astype(np.int32)
+        X, _ = tokens(T, H, "bf16", 60 + i)
+        if i == 3:
+            X[T - 1, 5] = float("inf")
+        if i == 4:
+            X[0, 9] = float("nan")
+        w = rng.standard_normal((T, k)).astype(np.float32)
+        w[:, k // 2] = 0.0
+        Y = poison((T, H), torch.float16)
+        w4.moe(X, torch.from_numpy(ids).to(DEV), torch.from_numpy(w).to(DEV), w13, w2, out=Y)
+        want, tol = ref.moe(X.float().cpu().numpy(), ids, w, W13, sw13, W2, sw2, "f16")
+        within(f64(Y), want, tol)
 
 
 def test_moe_same_as_its_steps():
@@ -363,6 +400,41 @@ def test_gemm_lora_extreme_values(M):
     assert np.isinf(got[big]).all() and (np.sign(got[big]) == np.sign(want[big])).all()
     sure = np.abs(want) < 65504 - tol
     within(got[sure], want[sure], tol[sure])
+
+
+@pytest.mark.parametrize("M,N", [(7, 512), (40, 512), (200, 512), (128, 256)])
+def test_gemm_lora_alignment(M, N):
+    """Vectors need 4-byte boundaries only: channel scales, adapter scales
+    and ids one element into their storage."""
+    X, p, lora, ad, want, tol = lora_case(M, N, 4096, 24, 5, 64, "f16", "any", 17)
+
+    def shifted(t):
+        s = torch.empty(t.numel() + 1, dtype=t.dtype, device=DEV)[1:]
+        s.copy_(t)
+        return s
+    got = w4.gemm_lora(X, dict(p, sw=shifted(p["sw"])), dict(lora, scale=shifted(lora["scale"])),
+                       shifted(ad))
+    within(f64(got), want, tol)
+
+
+@pytest.mark.parametrize("M", [16, 40, 300])
+def test_gemm_lora_rows_do_not_mix(M):
+    """An adapter with infinities and NaN, and rows that are not finite, leave
+    the rows of other adapters (in the same blocks) alone."""
+    X, p, lora, ad, _, _ = lora_case(M, 512, 512, 16, 4, 64, "bf16", "any", 19)
+    ad.copy_(torch.arange(M, device=DEV, dtype=torch.int32) % 5 - 1)
+    good = w4.gemm_lora(X, p, lora, ad)
+    assert torch.isfinite(good).all()
+    lora["A"][2, 3, 7] = float("inf")
+    lora["B"][2, 9] = float("nan")
+    lora["B"][1, 11, 2] = float("inf")
+    X[5] = float("nan")
+    bad = w4.gemm_lora(X, p, lora, ad)
+    ok = (ad != 2) & (ad != 1)
+    ok[5] = False
+    assert torch.equal(bad[ok], good[ok])
+    assert not torch.isfinite(bad[ad == 1][:, 11]).any()
+    assert not torch.isfinite(bad[ad == 2]).all(dim=1).any()
 
 
 def test_gemm_lora_adapters_past_4_gib():

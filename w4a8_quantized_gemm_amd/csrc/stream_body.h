@@ -335,7 +335,7 @@ __device__ __forceinline__ void stream_body(
             const bool live = m < row_hi;
             const int id = lora_id(lora, m, live);
             const float xs = live ? sx[m] : 0.0f;
-            const v4f ws = *reinterpret_cast<const v4f*>(sw + n + 4 * G);
+            const float* ws = sw + n + 4 * G;  // (4-byte aligned only)
             v4i sum = v4i{0, 0, 0, 0};
             for (int w = 0; w < ks; ++w)
                 sum += *reinterpret_cast<const v4i*>(
