@@ -77,11 +77,10 @@ __global__ __launch_bounds__(1024) void lora_inputs_kernel(
 }
 
 // INT8 of the rows of one workgroup of 16 waves: WPR waves a row, its elements
-// in registers (K <= 4096 WPR), maxima joined through LDS.
-template <int IN, int WPR>
+// in registers (K <= 512 CH WPR), maxima joined through LDS.
+template <int IN, int WPR, int CH>
 __device__ __forceinline__ void quant_rows16(const void* X, long long row0, int M, int K,
                                              uint8_t* Xq, float* sx) {
-    constexpr int CH = 8;
     __shared__ float part[16];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const long long m = row0 + wave / WPR;
@@ -128,14 +127,16 @@ __device__ __forceinline__ void quant_rows16(const void* X, long long row0, int 
 // two read X within a few microseconds of each other, so once from HBM.
 // Inner product: wave w takes the 64-wide K-tiles w, w + 16, ...  Matrix
 // instructions 16 x 16 x 32 take A as the first and X as the second operand
-// (lane (r, G): rank / row r, columns 8 G .. + 7 of a 32-wide step).  The
-// work of a block of rows is a list of jobs, one per adapter that occurs
-// among the rows and 16 of its ranks; a pass over K takes two jobs, and every
-// row keeps its own adapter's (a select).  The passes are bound by the cache:
-// every block of 16 rows reads its adapters' A again (2048 x 4096, rank 32:
-// 12 us without adapters, 16 with one, 27 with two per block; more loads in
-// flight and other column orders change nothing).
-template <int IN, int WPR>
+// (lane (r, G): rank / row r, columns 8 G .. + 7 of a 32-wide step).  Loads
+// have four neighbouring lanes on one row (64 bytes) and a lane permutation
+// through the LDS network brings them to that layout: loaded in it, every
+// lane was a cache access of its own and the cache the bound (2048 x 4096,
+// rank 32, two adapters in every block: 27 us; 18 now; 12 without adapters
+// or with one, whose pass hides behind the quantisation).  The work of a
+// block of rows is a list of jobs, one per adapter that occurs among the rows
+// and 16 of its ranks; a pass over K takes two jobs, and every row keeps its
+// own adapter's (a select).
+template <int IN, int WPR, int CH>
 __global__ __launch_bounds__(1024, 8) void lora_rows_kernel(
     const void* __restrict__ X, const void* __restrict__ A, const int* __restrict__ adapter,
     const float* __restrict__ scale, int n_adapters, int M, int K, int R,
@@ -143,7 +144,7 @@ __global__ __launch_bounds__(1024, 8) void lora_rows_kernel(
     const int blocks = (M + 15) / 16;
     if constexpr (WPR > 0) {
         if ((int)blockIdx.x >= blocks) {
-            quant_rows16<IN, WPR>(X, (long long)(blockIdx.x - blocks) * (16 / WPR), M, K, Xq, sx);
+            quant_rows16<IN, WPR, CH>(X, (long long)(blockIdx.x - blocks) * (16 / WPR), M, K, Xq, sx);
             return;
         }
     }
@@ -154,7 +155,17 @@ __global__ __launch_bounds__(1024, 8) void lora_rows_kernel(
     const int m = blockIdx.x * 16 + r;
     const bool live = m < M;
     const int id = live ? adapter[m] : -1;
-    const uint8_t* x = reinterpret_cast<const uint8_t*>(X) + ((size_t)(live ? m : 0) * K + 8 * G) * 2;
+    const int lr = lane >> 2, lc = 8 * (lane & 3);  // row and column this lane loads
+    const int from = 4 * (4 * r + G);               // and the lane whose load it uses
+    auto arrange = [&](v4i v) {
+        v4i o;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) o[q] = __builtin_amdgcn_ds_bpermute(from, v[q]);
+        return o;
+    };
+    // (a row past the end repeats the first: not kept)
+    const int mx = (int)blockIdx.x * 16 + lr < M ? (int)blockIdx.x * 16 + lr : 0;
+    const uint8_t* x = reinterpret_cast<const uint8_t*>(X) + ((size_t)mx * K + lc) * 2;
     unsigned rest = (unsigned)__ballot(id >= 0 && id < n_adapters) & 0xFFFFu;
     struct Job {
         int a, r0;
@@ -184,23 +195,24 @@ __global__ __launch_bounds__(1024, 8) void lora_rows_kernel(
         const uint8_t* ap[2];
 #pragma unroll
         for (int q = 0; q < 2; ++q) {  // ranks past R repeat the last: not kept
-            const int rr = min(job[q].r0 + r, R - 1);
+            const int rr = min(job[q].r0 + lr, R - 1);
             ap[q] = reinterpret_cast<const uint8_t*>(A) +
-                    (((size_t)job[both ? q : 0].a * R + (both || q == 0 ? rr : 0)) * K + 8 * G) * 2;
+                    (((size_t)job[both ? q : 0].a * R + (both || q == 0 ? rr : 0)) * K + lc) * 2;
         }
         for (int kt = wave; kt < KT; kt += 16) {
             v4i xv[2], av[2][2];
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 const size_t o = ((size_t)kt * 64 + 32 * i) * 2;
-                xv[i] = load16(x + o);  // a row past the end repeats row 0: not kept
+                xv[i] = load16(x + o);
                 av[0][i] = load16(ap[0] + o);
                 if (both) av[1][i] = load16(ap[1] + o);
             }
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                acc[0] = lora_mfma<IN>(av[0][i], xv[i], acc[0]);
-                if (both) acc[1] = lora_mfma<IN>(av[1][i], xv[i], acc[1]);
+                const v4i xo = arrange(xv[i]);
+                acc[0] = lora_mfma<IN>(arrange(av[0][i]), xo, acc[0]);
+                if (both) acc[1] = lora_mfma<IN>(arrange(av[1][i]), xo, acc[1]);
             }
         }
         __syncthreads();  // the previous pass's sums have been read
@@ -289,13 +301,25 @@ hipError_t inputs_run(const void* X, const void* A, const int* adapter, const fl
             hipError_t e = launch_act_int8(X, IN, M, K, Xq, sx, st);
             if (e != hipSuccess || n_adapters == 0) return e;
         }
-#define ROWS(WPR, ROWS_PER)                                                                      \
-    hipLaunchKernelGGL((lora_rows_kernel<IN, WPR>), dim3(blocks + ROWS_PER), dim3(1024), 0, st, X, \
-                       A, adapter, scale, n_adapters, M, K, R, q, sx, V)
-        if (K <= 4096) ROWS(1, (M + 15) / 16);
-        else if (K <= 8192) ROWS(2, (M + 7) / 8);
-        else if (K <= 16384) ROWS(4, (M + 3) / 4);
-        else ROWS(0, 0);
+        // waves per row: more for long rows, and until the rows fill 256 workgroups
+        int wpr = 1, ch = 2;
+        while (wpr < 4 && ((long long)M * wpr < 4096 || K > 4096 * wpr)) wpr *= 2;
+        while (512 * ch * wpr < K) ch *= 2;
+#define ROWS(WPR, CH)                                                                            \
+    hipLaunchKernelGGL((lora_rows_kernel<IN, WPR, CH>),                                          \
+                       dim3(blocks + (WPR ? (M * (long long)WPR + 15) / 16 : 0)), dim3(1024), 0, st, \
+                       X, A, adapter, scale, n_adapters, M, K, R, q, sx, V)
+#define ROWS_CH(WPR)               \
+    do {                           \
+        if (ch == 2) ROWS(WPR, 2); \
+        else if (ch == 4) ROWS(WPR, 4); \
+        else ROWS(WPR, 8);         \
+    } while (0)
+        if (K > 16384) ROWS(0, 2);
+        else if (wpr == 1) ROWS_CH(1);
+        else if (wpr == 2) ROWS_CH(2);
+        else ROWS_CH(4);
+#undef ROWS_CH
 #undef ROWS
         return hipGetLastError();
     }
