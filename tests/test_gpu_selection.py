@@ -352,6 +352,11 @@ LORA = [
     (1037, 1280, 640, 16, 5, 64, "bf16", "runs"),
     (520, 256, 16384, 16, 3, 128, "f16", "runs"),   # long K
     (2100, 4096, 512, 32, 3, 128, "bf16", "runs"),
+    # rows longer than the quantising kernels hold in registers; group
+    # parameters that do not fit in the streamed kernel's LDS
+    (5, 64, 33024, 8, 2, 64, "f16", "any"),
+    (513, 64, 16640, 24, 3, 128, "bf16", "any"),
+    (512, 256, 2048, 96, 6, 64, "f16", "any"),
 ]
 
 

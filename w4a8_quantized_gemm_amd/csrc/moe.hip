@@ -511,98 +511,98 @@ __global__ __launch_bounds__(256, 4) void moe_few_kernel(
         }
     };
     while (mine) {  // the next slots, at most cap (<= 16)
-    const int count = min(cap, __builtin_popcountll(mine));
-    Stage st[D];
+        const int count = min(cap, __builtin_popcountll(mine));
+        Stage st[D];
 #pragma unroll
-    for (int d = 0; d < D; ++d)
-        if (d < nk) issue(d, st[d]);
+        for (int d = 0; d < D; ++d)
+            if (d < nk) issue(d, st[d]);
 
-    // the rows, behind 16 bytes of zeros for the absent ones
-    const int stride = K + 16;
-    int8_t* rows = reinterpret_cast<int8_t*>(lds) + 16;
-    if (tid < 4) reinterpret_cast<int*>(lds)[tid] = 0;
-    constexpr int EB = IN == 0 ? 4 : 2;
-    for (int i = 0; i < count; ++i) {
-        const int slot = nth_bit(mine, i), row = HALVES == 2 ? slot / k : slot;
-        const float s =
-            quant_row_lds<IN>(true, reinterpret_cast<const uint8_t*>(X) + (size_t)row * K * EB, K,
-                              wave, WAVES, rows + i * stride, part);
-        if (tid == 0) scales[i] = s;
-        __syncthreads();
-    }
-    const int8_t* xrow = r < count ? rows + r * stride + 32 * G : nullptr;
-
-    v4i acc[TT];
-#pragma unroll
-    for (int t = 0; t < TT; ++t) acc[t] = v4i{0, 0, 0, 0};
-    auto consume = [&](int i, const Stage& S_) {
-        const int8_t* x = xrow ? xrow + (wave + WAVES * i) * kTileK : reinterpret_cast<int8_t*>(lds);
-        const v4i x0 = *reinterpret_cast<const v4i*>(x);
-        const v4i x1 = *reinterpret_cast<const v4i*>(xrow ? x + 16 : x);
-#pragma unroll
-        for (int t = 0; t < TT; ++t) {
-            const int b = (nt0 & 3) + t % NT;
-            const u16x2 s2 = scale_pair(S_.s[t / NT], b), a4 = offset_quad(S_.a[t / NT], b);
-            unsigned q[8];
-            lqq_dequant8((unsigned)S_.w[t].x, s2, a4, q[0], q[1]);
-            lqq_dequant8((unsigned)S_.w[t].y, s2, a4, q[2], q[3]);
-            lqq_dequant8((unsigned)S_.w[t].z, s2, a4, q[4], q[5]);
-            lqq_dequant8((unsigned)S_.w[t].w, s2, a4, q[6], q[7]);
-            acc[t] = __builtin_amdgcn_mfma_i32_16x16x64_i8(
-                x0, v4i{(int)q[0], (int)q[1], (int)q[2], (int)q[3]}, acc[t], 0, 0, 0);
-            acc[t] = __builtin_amdgcn_mfma_i32_16x16x64_i8(
-                x1, v4i{(int)q[4], (int)q[5], (int)q[6], (int)q[7]}, acc[t], 0, 0, 0);
+        // the rows, behind 16 bytes of zeros for the absent ones
+        const int stride = K + 16;
+        int8_t* rows = reinterpret_cast<int8_t*>(lds) + 16;
+        if (tid < 4) reinterpret_cast<int*>(lds)[tid] = 0;
+        constexpr int EB = IN == 0 ? 4 : 2;
+        for (int i = 0; i < count; ++i) {
+            const int slot = nth_bit(mine, i), row = HALVES == 2 ? slot / k : slot;
+            const float s =
+                quant_row_lds<IN>(true, reinterpret_cast<const uint8_t*>(X) + (size_t)row * K * EB, K,
+                                  wave, WAVES, rows + i * stride, part);
+            if (tid == 0) scales[i] = s;
+            __syncthreads();
         }
-    };
-    int i = 0;
-    for (; i + 2 * D <= nk; i += D) {
+        const int8_t* xrow = r < count ? rows + r * stride + 32 * G : nullptr;
+
+        v4i acc[TT];
+#pragma unroll
+        for (int t = 0; t < TT; ++t) acc[t] = v4i{0, 0, 0, 0};
+        auto consume = [&](int i, const Stage& S_) {
+            const int8_t* x = xrow ? xrow + (wave + WAVES * i) * kTileK : reinterpret_cast<int8_t*>(lds);
+            const v4i x0 = *reinterpret_cast<const v4i*>(x);
+            const v4i x1 = *reinterpret_cast<const v4i*>(xrow ? x + 16 : x);
+#pragma unroll
+            for (int t = 0; t < TT; ++t) {
+                const int b = (nt0 & 3) + t % NT;
+                const u16x2 s2 = scale_pair(S_.s[t / NT], b), a4 = offset_quad(S_.a[t / NT], b);
+                unsigned q[8];
+                lqq_dequant8((unsigned)S_.w[t].x, s2, a4, q[0], q[1]);
+                lqq_dequant8((unsigned)S_.w[t].y, s2, a4, q[2], q[3]);
+                lqq_dequant8((unsigned)S_.w[t].z, s2, a4, q[4], q[5]);
+                lqq_dequant8((unsigned)S_.w[t].w, s2, a4, q[6], q[7]);
+                acc[t] = __builtin_amdgcn_mfma_i32_16x16x64_i8(
+                    x0, v4i{(int)q[0], (int)q[1], (int)q[2], (int)q[3]}, acc[t], 0, 0, 0);
+                acc[t] = __builtin_amdgcn_mfma_i32_16x16x64_i8(
+                    x1, v4i{(int)q[4], (int)q[5], (int)q[6], (int)q[7]}, acc[t], 0, 0, 0);
+            }
+        };
+        int i = 0;
+        for (; i + 2 * D <= nk; i += D) {
+#pragma unroll
+            for (int d = 0; d < D; ++d) {
+                consume(i + d, st[d]);
+                issue(i + d + D, st[d]);
+                __builtin_amdgcn_sched_barrier(0);
+            }
+        }
 #pragma unroll
         for (int d = 0; d < D; ++d) {
-            consume(i + d, st[d]);
-            issue(i + d + D, st[d]);
-            __builtin_amdgcn_sched_barrier(0);
+            if (i + d < nk) {
+                consume(i + d, st[d]);
+                if (i + d + D < nk) issue(i + d + D, st[d]);
+            }
         }
-    }
 #pragma unroll
-    for (int d = 0; d < D; ++d) {
-        if (i + d < nk) {
-            consume(i + d, st[d]);
-            if (i + d + D < nk) issue(i + d + D, st[d]);
-        }
-    }
-#pragma unroll
-    for (int d = 0; d < D; ++d)
-        if (i + D + d < nk) consume(i + D + d, st[d]);
+        for (int d = 0; d < D; ++d)
+            if (i + D + d < nk) consume(i + D + d, st[d]);
 
-    __syncthreads();  // all waves have read the rows
-    int* red = reinterpret_cast<int*>(lds);
+        __syncthreads();  // all waves have read the rows
+        int* red = reinterpret_cast<int*>(lds);
 #pragma unroll
-    for (int t = 0; t < TT; ++t)
+        for (int t = 0; t < TT; ++t)
 #pragma unroll
-        for (int v = 0; v < 4; ++v) red[((wave * TT + t) * 4 + v) * 64 + lane] = acc[t][v];
-    __syncthreads();
-    for (int q = tid; q < NT * 256; q += 256) {
-        const int t = q >> 8, l = q & 63, row = 4 * (l >> 4) + ((q >> 6) & 3);
-        if (row >= count) continue;
-        const int n = (nt0 + t) * kTileN + (l & 15), slot = nth_bit(mine, row);
-        int sum[HALVES];
+            for (int v = 0; v < 4; ++v) red[((wave * TT + t) * 4 + v) * 64 + lane] = acc[t][v];
+        __syncthreads();
+        for (int q = tid; q < NT * 256; q += 256) {
+            const int t = q >> 8, l = q & 63, row = 4 * (l >> 4) + ((q >> 6) & 3);
+            if (row >= count) continue;
+            const int n = (nt0 + t) * kTileN + (l & 15), slot = nth_bit(mine, row);
+            int sum[HALVES];
 #pragma unroll
-        for (int hf = 0; hf < HALVES; ++hf) {
-            sum[hf] = 0;
-            for (int w = 0; w < WAVES; ++w) sum[hf] += red[(w * TT + hf * NT) * 256 + q];
+            for (int hf = 0; hf < HALVES; ++hf) {
+                sum[hf] = 0;
+                for (int w = 0; w < WAVES; ++w) sum[hf] += red[(w * TT + hf * NT) * 256 + q];
+            }
+            const float x = scales[row];
+            const float y = ((float)sum[0] * x) * sw[(size_t)e * N + n];
+            if constexpr (HALVES == 2) {
+                const float u = ((float)sum[HALVES - 1] * x) * sw[(size_t)e * N + nh + n];
+                out[(size_t)slot * nh + n] = y / (1.0f + expf(-y)) * u;
+            } else {
+                const float w = weights[slot];
+                out[(size_t)slot * N + n] = w != 0.0f ? w * y : 0.0f;
+            }
         }
-        const float x = scales[row];
-        const float y = ((float)sum[0] * x) * sw[(size_t)e * N + n];
-        if constexpr (HALVES == 2) {
-            const float u = ((float)sum[HALVES - 1] * x) * sw[(size_t)e * N + nh + n];
-            out[(size_t)slot * nh + n] = y / (1.0f + expf(-y)) * u;
-        } else {
-            const float w = weights[slot];
-            out[(size_t)slot * N + n] = w != 0.0f ? w * y : 0.0f;
-        }
-    }
-    for (int i = 0; i < count; ++i) mine &= mine - 1;
-    __syncthreads();  // the sums have been read
+        for (int i = 0; i < count; ++i) mine &= mine - 1;
+        __syncthreads();  // the sums have been read
     }
 }
 
