@@ -86,16 +86,13 @@ __device__ __forceinline__ void quant_row(const void* row, int K, int8_t* out, f
 #pragma unroll
         for (int j = 0; j < 8; ++j) m = MaxU32{}(m, abs_bits(r.v[j]));
     }
-    const float s = row_scale_bits(block_max_bits(m));
+    const float s = row_scale_bits(block_max_bits(m)), inv = __fdiv_rn(1.0f, s);
     if (threadIdx.x == 0) *scale = s;
-    uint2* o = reinterpret_cast<uint2*>(out);
     for (int i = threadIdx.x; i < K / 8; i += blockDim.x) {
         const Row8<IN> r = load_row8<IN>(row, i);
-        unsigned b[8];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) b[j] = (unsigned)(quant_sym(r.v[j], s, 127.0f) & 0xFF);
-        o[i] = uint2{b[0] | (b[1] << 8) | (b[2] << 16) | (b[3] << 24),
-                     b[4] | (b[5] << 8) | (b[6] << 16) | (b[7] << 24)};
+        reinterpret_cast<uint2*>(out)[i] =
+            uint2{quant4_fast(r.v[0], r.v[1], r.v[2], r.v[3], s, inv),
+                  quant4_fast(r.v[4], r.v[5], r.v[6], r.v[7], s, inv)};
     }
 }
 
@@ -174,8 +171,7 @@ __global__ __launch_bounds__(1024) void moe_quant_kernel(const float* __restrict
 // Workgroup -> group of channels.  Workgroups are dealt round-robin to the
 // eight XCDs: give b and b + 8 neighbouring groups, so that a panel of group
 // parameters (64 channels) is read into one XCD's L2.
-__device__ __forceinline__ int channel_group() {
-    const int n = gridDim.x, b = blockIdx.x;
+__device__ __forceinline__ int channel_group(int b, int n) {
     return (n & 7) ? b : (b & 7) * (n >> 3) + (b >> 3);
 }
 
@@ -184,7 +180,8 @@ __device__ __forceinline__ int channel_group() {
 // HALVES = 1: the down product, scaled by the slot's weight, into part[slot].
 // blockIdx.x: channel group, blockIdx.y: index into the active experts.  The
 // `ks` waves take interleaved K-tiles and are summed in LDS (exact int32).
-// Up to 16 RB rows share each decoded weight; more rows repeat the stream.
+// Up to 16 RB rows share each decoded weight; the rows of an expert with more
+// are dealt to the workgroups of blockIdx.z, and past those repeat the stream.
 template <int HALVES, int NT, int RB, int D, int GROUP>
 __global__ __launch_bounds__(512) void moe_product_kernel(
     const int8_t* __restrict__ Xq, const float* __restrict__ sx, const uint8_t* __restrict__ wq,
@@ -203,7 +200,9 @@ __global__ __launch_bounds__(512) void moe_product_kernel(
     const int KT = K / kTileK, groups = K / GROUP;
     const size_t e = act.expert;
     const int nh = N / HALVES;  // channels of one half
-    const int nt0 = channel_group() * NT;
+    const int part = blockIdx.z, sharers = gridDim.z;
+    if (16 * RB * part >= act.count) return;
+    const int nt0 = channel_group(blockIdx.x, gridDim.x) * NT;
     const int nk = wave < KT ? (KT - wave + ks - 1) / ks : 0;
     auto kt_of = [&](int i) { return wave + ks * i; };
 
@@ -225,7 +224,7 @@ __global__ __launch_bounds__(512) void moe_product_kernel(
         v4i x0[RB], x1[RB], w[TT];
         unsigned s[HALVES], a[HALVES];
     };
-    for (int r0 = 0; r0 < act.count; r0 += 16 * RB) {
+    for (int r0 = 16 * RB * part; r0 < act.count; r0 += 16 * RB * sharers) {
         // Rows (lane / 8) and 8 + (lane / 8) of row block rb, 16-byte piece
         // lane % 8: the row's token (W13) or its own place (W2).  Absent rows
         // get an offset past the buffer, which reads 0.
@@ -481,7 +480,7 @@ __global__ __launch_bounds__(256, 4) void moe_few_kernel(
     unsigned long long mine = readlane64(f.peers, first);  // its slots
 
     const int nh = N / HALVES;  // channels of one half
-    const int KT = K / kTileK, groups = K / GROUP, nt0 = channel_group() * NT;
+    const int KT = K / kTileK, groups = K / GROUP, nt0 = channel_group(blockIdx.x, gridDim.x) * NT;
     const int nk = wave < KT ? (KT - wave + WAVES - 1) / WAVES : 0;
     const __amdgpu_buffer_rsrc_t w_rsrc =
         buf_rsrc(wq + (size_t)e * ((size_t)N * K / 2), (unsigned)((size_t)N * K / 2));
@@ -627,7 +626,7 @@ __global__ __launch_bounds__(1024) void moe_few_down_kernel(
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int r = lane & 15, G = lane >> 4;
     const FewSlots f = few_slots(ids, S, E);
-    const int KT = K / kTileK, groups = K / GROUP, nt = channel_group();
+    const int KT = K / kTileK, groups = K / GROUP, nt = channel_group(blockIdx.x, gridDim.x);
     const int nk = wave < KT ? (KT - wave + WAVES - 1) / WAVES : 0;
     const int total = nk * __builtin_popcountll(f.first);
     const size_t wbytes = (size_t)H * K / 2, pbytes = (size_t)H * groups;
@@ -789,15 +788,27 @@ float most_rows(int T, int S, int E) {
 // (the two-launch form lost to three from two tokens on: 22.1 against 21.1).
 constexpr size_t kFewLds = 40 * 1024;
 
-// Row blocks of 16 that share a decoded weight (an expert with more rows
-// repeats its stream).  us with one / two / four blocks:
-//   131 tokens, two of 16 experts 6400 x 4096:   200 / 163 / 172
-//   48 tokens, two of 8 experts 4096 x 2048:     47.8 / 41.6 / 49.3
-//   200 tokens, the same:                        119.9 / 95.1 / 90.1
-//   64 tokens, six of 64 experts 1408 x 2048:    71.9 / 71.9 / 109
+// Row blocks of 16 that share a decoded weight.  us with one / two / four
+// blocks (means of two routings):
+//   24 tokens, two of 8 experts 4096 x 2048 (6 slots per expert): 36.7 / 38.5 / 47
+//   32 tokens, two of 8 experts 14336 x 4096 (8):                 140 / 142 / 186
+//   48 tokens, two of 8 experts 4096 x 2048 (12):                 46.4 / 42.4 / 50.7
+//   131 tokens, two of 16 experts 6400 x 4096 (16):               186 / 148 / 187
+//   200 tokens, two of 8 experts 4096 x 2048 (50):                87.7 / 69.8 / 76.7
+//   250 tokens, two of 8 experts 6400 x 4096 (62):                275 / 183 / 172
 int row_blocks(int T, int S, int E) {
-    const float most = most_rows(T, S, E);
-    return most <= 20.0f ? 1 : most <= 40.0f ? 2 : 4;
+    return most_rows(T, S, E) <= 18.0f ? 1 : (float)S <= 56.0f * (float)E ? 2 : 4;
+}
+
+// Workgroups that share an expert's rows where they exceed the blocks: routing
+// is uneven (131 tokens, two of 16 experts, up to 50 of 262 slots on one: 170
+// us with one, 155 with these), and one that finds no rows of its own leaves
+// at once.  They come last in the grid: interleaved with the others, two or
+// four of them left half or most of the CUs idle (209 and 361 us), since
+// consecutive workgroups are dealt to the shader engines in turn.
+int row_sharers(int T, int rb) {
+    const int all = (T + 16 * rb - 1) / (16 * rb);
+    return all < 4 ? all : 4;
 }
 
 // Two tiles of each half per workgroup.  Waves splitting K: four, eight for
@@ -806,10 +817,10 @@ int row_blocks(int T, int S, int E) {
 template <int HALVES, int RB, int D>
 void launch_product(const int8_t* xq, const float* sx, const MoeWeights& w, const float* weights,
                     const MoeHead* head, const int* slots, float* out, int N, int K, int k,
-                    int rows_in, int experts, int group, hipStream_t st) {
+                    int rows_in, int experts, int group, int sharers, hipStream_t st) {
     constexpr int NT = 2;
     const int ks = HALVES == 1 && RB == 1 && K >= 64 * kTileK ? 8 : 4;
-    const dim3 grid(N / HALVES / (kTileN * NT), experts), block(64 * ks);
+    const dim3 grid(N / HALVES / (kTileN * NT), experts, sharers), block(64 * ks);
     // X slots, then the sums of one row block
     const size_t xbytes = (size_t)ks * 2048 * RB;
     const size_t rbytes = (size_t)ks * HALVES * NT * 256 * sizeof(int);
@@ -924,20 +935,26 @@ hipError_t launch_moe(const void* X, int in_type, const int* ids, const float* w
     else if (in_type == 2) PREPARE(2);
     else PREPARE(0);
 #undef PREPARE
-    const int rb = row_blocks(T, S, E);
+    const int rb = row_blocks(T, S, E), sharers = row_sharers(T, rb);
     if (rb == 1)
-        launch_product<2, 1, 2>(xq, sx, w13, weights, head, slots, h, 2 * F, H, k, T, experts, group, st);
+        launch_product<2, 1, 2>(xq, sx, w13, weights, head, slots, h, 2 * F, H, k, T, experts, group,
+                                sharers, st);
     else if (rb == 2)
-        launch_product<2, 2, 1>(xq, sx, w13, weights, head, slots, h, 2 * F, H, k, T, experts, group, st);
+        launch_product<2, 2, 1>(xq, sx, w13, weights, head, slots, h, 2 * F, H, k, T, experts, group,
+                                sharers, st);
     else
-        launch_product<2, 4, 1>(xq, sx, w13, weights, head, slots, h, 2 * F, H, k, T, experts, group, st);
+        launch_product<2, 4, 1>(xq, sx, w13, weights, head, slots, h, 2 * F, H, k, T, experts, group,
+                                sharers, st);
     hipLaunchKernelGGL(moe_quant_kernel, dim3(S), dim3(1024), 0, st, h, F, head, hq, sh);
     if (rb == 1)
-        launch_product<1, 1, 2>(hq, sh, w2, weights, head, slots, part, H, F, k, S, experts, group, st);
+        launch_product<1, 1, 2>(hq, sh, w2, weights, head, slots, part, H, F, k, S, experts, group,
+                                sharers, st);
     else if (rb == 2)
-        launch_product<1, 2, 2>(hq, sh, w2, weights, head, slots, part, H, F, k, S, experts, group, st);
+        launch_product<1, 2, 2>(hq, sh, w2, weights, head, slots, part, H, F, k, S, experts, group,
+                                sharers, st);
     else
-        launch_product<1, 4, 2>(hq, sh, w2, weights, head, slots, part, H, F, k, S, experts, group, st);
+        launch_product<1, 4, 2>(hq, sh, w2, weights, head, slots, part, H, F, k, S, experts, group,
+                                sharers, st);
     launch_combine(part, ids, T, E, k, H, Y, out_type, st);
     return hipGetLastError();
 }
