@@ -74,7 +74,7 @@ typedef enum {
     W4A8_ERR_NULL_PTR = 1,    /* a required pointer is NULL                     */
     W4A8_ERR_SHAPE = 2,       /* negative size, K % 128, N % 64, group, qmax     */
     W4A8_ERR_ALIGNMENT = 3,   /* a pointer breaks the alignment rule above       */
-    W4A8_ERR_WORKSPACE = 4,   /* workspace smaller than w4a8_workspace_size()    */
+    W4A8_ERR_WORKSPACE = 4,   /* workspace smaller than the call's size function */
     W4A8_ERR_UNSUPPORTED = 5, /* device is not gfx950, or a bad mode/flag value  */
     W4A8_ERR_HIP = 6          /* a HIP call failed; see w4a8_last_hip_error()    */
 } w4a8_status_t;
@@ -384,8 +384,8 @@ w4a8_status_t w8a8_gemm(const int8_t* X, const float* sx, const int8_t* wq8,
 
 /*
  * Top-k gating of router logits and the grouping of the chosen slots.
- *   logits: [T][E] elements of in_type (W4A8_IN_*), 16-byte aligned, widened
- *     to float32 (exact).  An expert whose logit is -inf or NaN is not
+ *   logits: [T][E] elements of in_type (W4A8_IN_*), aligned to an element,
+ *     widened to float32 (exact).  An expert whose logit is -inf or NaN is not
  *     available to that token.
  *   ids[t][j]     int32 [T][k]: the expert with the j-th largest logit (ties
  *     go to the lowest index), -1 where fewer than j+1 are available;

@@ -92,6 +92,18 @@ def test_route(T, E, k, dt, renorm):
     within(f64(out["weights"]), w, tol)
 
 
+@pytest.mark.parametrize("T,E,dt", [(5, 7, "bf16"), (100, 33, "f16"), (9, 5, "f32")])
+def test_route_part_of_a_batch(T, E, dt):
+    """Rows of a larger batch: logits aligned to an element only."""
+    x = route_logits(T + 1, E, dt, 77)
+    out = w4.route(x.to(DEV)[1:], 3)
+    ids, w, tol, offsets, rows = ref.route(x[1:].to(torch.float64).numpy(), 3, True)
+    np.testing.assert_array_equal(host(out["ids"]), ids)
+    np.testing.assert_array_equal(host(out["rows"]), rows)
+    np.testing.assert_array_equal(host(out["offsets"]), offsets)
+    within(f64(out["weights"]), w, tol)
+
+
 def test_route_no_tokens():
     out = w4.route(torch.empty((0, 8), device=DEV), 2)
     assert host(out["offsets"]).tolist() == [0] * 9
@@ -209,11 +221,11 @@ def test_moe_odd_ids_and_rows():
     assert (f64(Y) == 0).all()
 
 
-@pytest.mark.parametrize("T,k", [(1, 6), (1, 16), (5, 4), (8, 8), (16, 4)])
-def test_moe_few_slots_odd_ids(T, k):
-    """The forms for few slots: ids outside the experts, an expert many times
-    over (more rows than a stream serves at once), zero and negative weights,
-    tokens that are not finite, calls without any expert."""
+@pytest.mark.parametrize("T,k", [(1, 6), (1, 16), (5, 4), (8, 8), (16, 4), (100, 3)])
+def test_moe_odd_ids_at_every_form(T, k):
+    """One token, few slots, many: ids outside the experts, an expert many
+    times over (more rows than a stream serves at once), zero and negative
+    weights, tokens that are not finite, calls without any expert."""
     E, H, F, g = 12, 256, 384, 64
     rng = np.random.default_rng(40 + T + k)
     w13, W13, sw13 = experts(E, 2 * F, H, g, 3500)
@@ -221,7 +233,7 @@ def test_moe_few_slots_odd_ids(T, k):
     cases = [np.full((T, k), 7), rng.integers(-2, E + 2, (T, k)), np.full((T, k), -1),
              rng.integers(0, 2, (T, k)) * 9, np.where(rng.random((T, k)) < 0.7, 3, 1 << 30)]
     for i, ids in enumerate(cases):
-        say(f"moe few T={T} k={k} ids {i}")
+        say(f"moe ids T={T} k={k} case {i}")
         ids = ids.astype(np.int32)
         X, _ = tokens(T, H, "bf16", 60 + i)
         if i == 3:

@@ -25,7 +25,8 @@ def test_route_refusals():
     for p in ("x", "ids", "w", "off", "rows"):
         assert route(**{p: None}) == NULL, p
     assert route(T=0, off=None) == NULL
-    assert route(x=A + 8) == ALIGN
+    assert route(x=A + 2) == ALIGN and route(x=A + 1, it=1) == ALIGN
+    assert route(x=A + 1, it=2) == ALIGN
     for p in ("ids", "w", "off", "rows"):
         assert route(**{p: A + 2}) == ALIGN, p
     need = lib.w4a8_route_workspace_size(1000, 64, 6)

@@ -512,8 +512,9 @@ W4A8_EXPORT w4a8_status_t w4a8_route(const void* logits, int in_type, int T, int
         return W4A8_ERR_UNSUPPORTED;
     if (!valid_route(T, E, k)) return W4A8_ERR_SHAPE;
     if (!offsets || (T > 0 && (!logits || !ids || !weights || !rows))) return W4A8_ERR_NULL_PTR;
+    const uintptr_t element = in_type == W4A8_IN_F32 ? 4 : 2;
     if (!aligned4(offsets) || !aligned4(ids) || !aligned4(weights) || !aligned4(rows) ||
-        !aligned16(logits))
+        reinterpret_cast<uintptr_t>(logits) % element != 0)
         return W4A8_ERR_ALIGNMENT;
     const size_t need = w4a8_route_workspace_size(T, E, k);
     if (workspace_bytes < need) return W4A8_ERR_WORKSPACE;
