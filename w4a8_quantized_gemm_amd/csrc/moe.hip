@@ -358,6 +358,9 @@ __global__ __launch_bounds__(512) void moe_product_kernel(
                 }
             }
         }
+        // the sums lie over the X slots: all of them are added up before the
+        // next rows' tiles go there
+        __syncthreads();
     }
 }
 
