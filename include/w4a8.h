@@ -449,8 +449,9 @@ w4a8_status_t w4a8_moe(const void* X, int in_type, const int32_t* ids,
  *                    + scale[a] * (X[m] . A[a]^T) . B[a]^T ),  a = adapter[m]
  * acc as w4a8_gemm on the INT8 rows (Xq, sx) that w4a8_quant_act_ex gives
  * for X; the adapter's products are float32 sums over the stored values, the
- * inner one kept as two numbers of in_type (16 significant bits; for fp16
- * at least 2^-38 of the largest of 32 ranks), and Y is rounded once.
+ * inner one held in float32 (the outer one meets it as it is for bfloat16,
+ * for fp16 within 2^-23, one unit in its last place, or 2^-50 of the largest
+ * of 32 ranks), and Y is rounded once.
  *   X: [M][K], A: [n_adapters][R][K], B: [n_adapters][N][R], all fp16 or all
  *     bfloat16 (in_type); scale: float32 [n_adapters]; adapter: int32 [M],
  *     values outside [0, n_adapters) select none, in any order.  Adapters of

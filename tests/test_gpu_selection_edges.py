@@ -57,3 +57,68 @@ def test_moe_hot_expert(T, E, k, H, F, g, dt, distinct):
     want, tol = ref.moe(Xf, ids, w, W13, sw13, W2, sw2, dt)
     within(f64(outs[0]), want, tol)
     assert all(torch.equal(o, outs[0]) for o in outs[1:])
+
+
+# ------------------------------------------------------------------- lora ---
+# streamed (one and several row blocks), K split, 128- and 256-row tiles with
+# one, two and four sets of 32 ranks
+PATHS = [(5, 320, 256, 8), (40, 512, 384, 16), (100, 192, 256, 40), (128, 512, 4096, 40),
+         (130, 768, 256, 72), (300, 768, 640, 16), (2100, 4096, 512, 40), (2100, 4096, 512, 104)]
+
+
+def bare(M, N, K, R, n, dt, seed):
+    """A projection of zero weights (its sums are exactly 0), adapter choices
+    and empty rows and adapters to fill in."""
+    p = w4.pack(torch.zeros((N, K), device=DEV), group=64)
+    rng = np.random.default_rng(seed)
+    ad = rng.integers(-1, n, M).astype(np.int32)
+    X, A, B = np.zeros((M, K)), np.zeros((n, R, K)), np.zeros((n, N, R))
+    return p, rng, ad, X, A, B
+
+
+def adapters(p, X, A, B, ad, dt):
+    """gemm_lora of float64 arrays whose values the type holds exactly."""
+    def dev(a):
+        t = torch.from_numpy(a).to(TYPES[dt])
+        same = t.double().numpy()
+        assert np.array_equal(same, a, equal_nan=True)
+        return t.to(DEV)
+    lora = {"A": dev(A), "B": dev(B), "scale": torch.ones(len(A), device=DEV)}
+    return f64(w4.gemm_lora(dev(X), p, lora, torch.from_numpy(ad).to(DEV)))
+
+
+@pytest.mark.parametrize("dt", ["f16", "bf16"])
+@pytest.mark.parametrize("M,N,K,R", PATHS)
+def test_lora_inner_product_is_kept_in_float32(M, N, K, R, dt):
+    """Inner products of 24 significant bits that cancel in the outer one.
+
+    Each is a sum of three 8-bit numbers 2^-8 apart, so every float32 sum that
+    forms it is exact; a channel takes the difference of two that agree in
+    their first 16 bits, next to one 2^26 times as large that it does not
+    take.  What is left are the roundings of the outer sum, of two products of
+    at most three parts each (six additions of u, and 2 u for parts that fall
+    short of the number by one unit in its last place), and the output's."""
+    say(f"lora bits M={M} N={N} K={K} R={R} {dt}")
+    n = 3
+    p, rng, ad, X, A, B = bare(M, N, K, R, n, dt, M + R)
+    X[:, :4] = [2.0 ** 12, 2.0 ** -2, 2.0 ** -6, 2.0 ** -10]
+
+    def eight(*shape):
+        return rng.integers(128, 256, shape) / 128.0
+    A[:, :, 1] = np.repeat(eight(n, R // 2), 2, axis=1)
+    A[:, :, 2] = np.repeat(eight(n, R // 2), 2, axis=1) * 2.0 ** -4
+    A[:, :, 3] = eight(n, R) * 2.0 ** -8
+    A[:, ::32, 0] = 2.0 ** 12
+    pairs = np.array([r for r in range(0, R, 2) if r % 32])
+    first = pairs[np.arange(N) % len(pairs)]
+    for a in range(n):
+        B[a, np.arange(N), first] = 2.0 ** 10
+        B[a, np.arange(N), first + 1] = -2.0 ** 10
+    got = adapters(p, X, A, B, ad, dt)
+    want, size = np.zeros((M, N)), np.zeros((M, N))
+    for a in range(n):
+        V = X @ A[a].T
+        m = ad == a
+        want[m] = V[m] @ B[a].T
+        size[m] = np.abs(V[m]) @ np.abs(B[a]).T
+    within(got, want, 8 * ref.U * size + ref.rounding(want, "f16"))

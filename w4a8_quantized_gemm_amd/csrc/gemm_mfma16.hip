@@ -159,13 +159,14 @@ __device__ __forceinline__ void mfma16_drain(v4i (&acc)[RB][4]) {
 }  // namespace
 
 // LDS of a workgroup whose epilogue adds low-rank adapters: per row its
-// adapter (-1: none), scale and operands of the first 32 ranks (8 pieces of
-// 16 bytes, high and low parts of each 8 ranks, and one piece of padding),
-// per channel its scale.
-constexpr unsigned kLoraVStride = 8 * 16 + 16;
+// adapter (-1: none), scale and operands of the first 32 ranks (a piece of
+// 16 bytes per 8 ranks and operand part, and one piece of padding), per
+// channel its scale.
+template <int LORA>
+constexpr unsigned kLoraVStride = 4 * LoraV<LORA>::PARTS * 16 + 16;
 template <int MT, int LORA>
 struct LoraLds {
-    uint8_t v[MT * kLoraVStride];
+    uint8_t v[MT * kLoraVStride<LORA>];
     float backs[LORA == 1 ? MT * 4 : 4];  // [32 ranks][row]
     float sx[MT], sw[kNT];
     int ids[MT];
@@ -184,10 +185,11 @@ __device__ __forceinline__ void lora_stage_v(const LoraArgs& lora, int m0, int r
 #pragma unroll
             for (int j = 0; j < 8; ++j) v[j] = p[j >> 2][j & 3];
         }
-        const LoraV o = lora_split<LORA, 1, 2>(v);
-        v4i* d = reinterpret_cast<v4i*>(dst + (unsigned)((s - s0) * MT + row) * kLoraVStride);
-        d[2 * (i & 3)] = o.hi;
-        d[2 * (i & 3) + 1] = o.lo;
+        const LoraV<LORA> o = lora_split<LORA, 1, 2>(v);
+        constexpr int P = LoraV<LORA>::PARTS;
+        v4i* d = reinterpret_cast<v4i*>(dst + (unsigned)((s - s0) * MT + row) * kLoraVStride<LORA>);
+#pragma unroll
+        for (int p = 0; p < P; ++p) d[P * (i & 3) + p] = o.part[p];
         if (LORA == 1 && (i & 3) == 0) backs[s * MT + row] = o.back;
     }
 }
@@ -237,7 +239,7 @@ __device__ __forceinline__ void mfma16_lora_epilogue(v4i (&acc)[MT / 16][4], uin
     const int r = lane & 15, G = lane >> 4;
     // ranks past the first 32: behind the staging blocks where they fit
     const int ns = (lora.R + 31) / 32;
-    const bool v_in_lds = VOFF + (unsigned)(MT * (ns - 1)) * kLoraVStride <= lds_bytes;
+    const bool v_in_lds = VOFF + (unsigned)(MT * (ns - 1)) * kLoraVStride<LORA> <= lds_bytes;
     if (v_in_lds && ns > 1) {
         lora_stage_v<MT, LORA>(lora, m0, row_hi, 1, ns, lds + VOFF, pre.backs);
         __syncthreads();
@@ -278,10 +280,15 @@ __device__ __forceinline__ void mfma16_lora_epilogue(v4i (&acc)[MT / 16][4], uin
                         return lora_split<LORA>(v);
                     }
                     const uint8_t* base =
-                        s == 0 ? pre.v : lds + VOFF + (unsigned)((s - 1) * MT) * kLoraVStride;
-                    const v4i* q = reinterpret_cast<const v4i*>(base + (unsigned)row * kLoraVStride);
-                    return LoraV{q[2 * G], q[2 * G + 1],
-                                 LORA == 1 ? pre.backs[s * MT + row] : 1.0f};
+                        s == 0 ? pre.v : lds + VOFF + (unsigned)((s - 1) * MT) * kLoraVStride<LORA>;
+                    const v4i* q =
+                        reinterpret_cast<const v4i*>(base + (unsigned)row * kLoraVStride<LORA>);
+                    LoraV<LORA> o;
+                    constexpr int P = LoraV<LORA>::PARTS;
+#pragma unroll
+                    for (int k = 0; k < P; ++k) o.part[k] = q[P * G + k];
+                    o.back = LORA == 1 ? pre.backs[s * MT + row] : 1.0f;
+                    return o;
                 },
                 held, y[p]);
         }

@@ -4,12 +4,15 @@
 // A 16 x 16 block (16 channels, 16 rows of X) takes one 16 x 16 x 32 matrix
 // instruction per 32 ranks and operand part.  B is used as stored (fp16 or
 // bfloat16, 16 bytes per lane straight from memory); V is float32 and is
-// split into two operands of B's type, V = hi + lo, each rounded to nearest:
-//   bfloat16: hi + lo keeps 16 significant bits of each element;
+// split into operands of B's type, each rounded to nearest:
+//   bfloat16: three parts of 8 bits, V exactly (two, 16 bits of V, took 754 us
+//     against 760 at 4096 x 28672 x 8192, rank 16, and 22.9 against 23.4 at
+//     47 x 11008 x 4096, rank 64);
 //   fp16: the 32 ranks of a row are first scaled by a power of two that
-//     brings their largest to [2^14, 2^15) (its range would lose V
-//     otherwise), hi + lo then keeps 21 bits, or 2^-38 of the largest for
-//     elements far below it.
+//     brings their largest to [2^14, 2^15) (V's range is not fp16's), then
+//     split into two parts, the second times 2^11 so that it keeps its bits
+//     where the first is subnormal.  V is met within 2^-23, one unit in its
+//     last place, or 2^-50 of the largest of the 32 ranks.
 // Sums are float32.  Rows of a block may select different adapters: the
 // block is multiplied by each adapter that occurs in it and every row keeps
 // its own product (a select, so another row's infinities do not reach it).
@@ -32,18 +35,24 @@ __device__ __forceinline__ v4f lora_mfma(v4i a, v4i b, v4f c) {
                                                        __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
 }
 
-// Operand parts of 8 ranks of one row, and the factor of their products.
+// Operand parts of 8 ranks of one row, the smallest first, and the factor of
+// their products.
+template <int IN>
 struct LoraV {
-    v4i hi, lo;
+    static constexpr int PARTS = IN == 1 ? 2 : 3;
+    v4i part[PARTS];
     float back;
 };
+// fp16: the second part's factor, taken back in the sums.
+constexpr float kLoraLow = 2048.0f;
 
 // v: 8 of a row's 32 ranks; the lanes that hold the other 24 are this lane's
 // number with the bits X1 and X2 flipped.
 template <int IN, int X1 = 16, int X2 = 32>
-__device__ __forceinline__ LoraV lora_split(const float (&v)[8]) {
-    LoraV o;
-    unsigned h[8], l[8];
+__device__ __forceinline__ LoraV<IN> lora_split(const float (&v)[8]) {
+    LoraV<IN> o;
+    constexpr int P = LoraV<IN>::PARTS;
+    unsigned h[P][8];
     if constexpr (IN == 1) {
         unsigned m = 0;
 #pragma unroll
@@ -65,23 +74,27 @@ __device__ __forceinline__ LoraV lora_split(const float (&v)[8]) {
             const float x = v[j] * to;
             const _Float16 a = (_Float16)x;
             const float d = x - (float)a;  // NaN where a is infinite: no low part then
-            const _Float16 b = (_Float16)(d == d ? d : 0.0f);
-            h[j] = __builtin_bit_cast(unsigned short, a);
-            l[j] = __builtin_bit_cast(unsigned short, b);
+            const _Float16 b = (_Float16)(d == d ? d * kLoraLow : 0.0f);
+            h[1][j] = __builtin_bit_cast(unsigned short, a);
+            h[0][j] = __builtin_bit_cast(unsigned short, b);
         }
     } else {
         o.back = 1.0f;
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-            h[j] = __builtin_bit_cast(unsigned short, (__bf16)v[j]);  // to nearest even
-            const float d = v[j] - __builtin_bit_cast(float, h[j] << 16);
-            l[j] = __builtin_bit_cast(unsigned short, (__bf16)(d == d ? d : 0.0f));
+            float d = v[j];
+#pragma unroll
+            for (int p = P - 1; p >= 0; --p) {
+                h[p][j] = __builtin_bit_cast(unsigned short, (__bf16)d);  // to nearest even
+                d -= __builtin_bit_cast(float, h[p][j] << 16);
+                d = d == d ? d : 0.0f;
+            }
         }
     }
-    o.hi = v4i{(int)(h[0] | h[1] << 16), (int)(h[2] | h[3] << 16), (int)(h[4] | h[5] << 16),
-               (int)(h[6] | h[7] << 16)};
-    o.lo = v4i{(int)(l[0] | l[1] << 16), (int)(l[2] | l[3] << 16), (int)(l[4] | l[5] << 16),
-               (int)(l[6] | l[7] << 16)};
+#pragma unroll
+    for (int p = 0; p < P; ++p)
+        o.part[p] = v4i{(int)(h[p][0] | h[p][1] << 16), (int)(h[p][2] | h[p][3] << 16),
+                        (int)(h[p][4] | h[p][5] << 16), (int)(h[p][6] | h[p][7] << 16)};
     return o;
 }
 
@@ -117,44 +130,60 @@ __device__ __forceinline__ int lora_id(const LoraArgs& L, int m, bool live) {
     return a >= 0 && a < L.n_adapters ? a : -1;
 }
 
+// t[c] += the products of four channel blocks and one operand part (fp16) or
+// all three (bfloat16), inside a tile kernel, whose accumulators fill the
+// AGPRs.  There the compiler would give these instructions AGPR operands too
+// and move accumulators out of their way (and, where it runs out of
+// registers, has stored an accumulator incompletely), so they are issued in
+// assembly on VGPRs: five wait states for the operands, the dependent
+// instructions four apart, and 20 wait states (see mfma_loop_exit_wait)
+// before anything reads the results or overwrites the operands.
+#define LORA_MFMA4(OP, V)                                                                        \
+    OP " %0, %4, " V ", %0\n\t" OP " %1, %5, " V ", %1\n\t" OP " %2, %6, " V ", %2\n\t" OP        \
+       " %3, %7, " V ", %3\n\t"
+#define LORA_MFMA4_WAIT "s_nop 7\n\ts_nop 7\n\ts_nop 3"
+__device__ __forceinline__ void lora_mfma4_f16(const v4i (&b)[4], v4i v, v4f (&t)[4]) {
+    asm volatile("s_nop 4\n\t" LORA_MFMA4("v_mfma_f32_16x16x32_f16", "%8") LORA_MFMA4_WAIT
+                 : "+&v"(t[0]), "+&v"(t[1]), "+&v"(t[2]), "+&v"(t[3])
+                 : "v"(b[0]), "v"(b[1]), "v"(b[2]), "v"(b[3]), "v"(v));
+}
+__device__ __forceinline__ void lora_mfma4_bf16(const v4i (&b)[4], const v4i (&v)[3],
+                                                v4f (&t)[4]) {
+    asm volatile("s_nop 4\n\t" LORA_MFMA4("v_mfma_f32_16x16x32_bf16", "%8")
+                     LORA_MFMA4("v_mfma_f32_16x16x32_bf16", "%9")
+                         LORA_MFMA4("v_mfma_f32_16x16x32_bf16", "%10") LORA_MFMA4_WAIT
+                 : "+&v"(t[0]), "+&v"(t[1]), "+&v"(t[2]), "+&v"(t[3])
+                 : "v"(b[0]), "v"(b[1]), "v"(b[2]), "v"(b[3]), "v"(v[0]), "v"(v[1]), "v"(v[2]));
+}
+#undef LORA_MFMA4_WAIT
+#undef LORA_MFMA4
+
 // y[c] += the product of NC channel blocks for one adapter: bfloat16
 // accumulates onto y in the matrix core, fp16 is scaled back and added.
-// TILE: inside a tile kernel, whose accumulators fill the AGPRs.  There the
-// compiler would give these instructions AGPR operands too and move
-// accumulators out of their way (and, where it runs out of registers, has
-// stored an accumulator incompletely), so they are issued in assembly on
-// VGPRs: five wait states for the operands, the dependent halves four
-// instructions apart, and 20 wait states (see mfma_loop_exit_wait) before
-// anything reads the results or overwrites the operands.
-template <int IN>
-__device__ __forceinline__ void lora_mfma4_asm(const v4i (&b)[4], const LoraV& V, v4f (&t)[4]) {
-#define LORA_MFMA4_ASM(OP)                                                                       \
-    asm volatile("s_nop 4\n\t" OP " %0, %4, %8, %0\n\t" OP " %1, %5, %8, %1\n\t" OP           \
-                 " %2, %6, %8, %2\n\t" OP " %3, %7, %8, %3\n\t" OP " %0, %4, %9, %0\n\t" OP     \
-                 " %1, %5, %9, %1\n\t" OP " %2, %6, %9, %2\n\t" OP " %3, %7, %9, %3\n\t"         \
-                 "s_nop 7\n\ts_nop 7\n\ts_nop 3"                                                \
-                 : "+v"(t[0]), "+v"(t[1]), "+v"(t[2]), "+v"(t[3])                                \
-                 : "v"(b[0]), "v"(b[1]), "v"(b[2]), "v"(b[3]), "v"(V.lo), "v"(V.hi))
-    if constexpr (IN == 1)
-        LORA_MFMA4_ASM("v_mfma_f32_16x16x32_f16");
-    else
-        LORA_MFMA4_ASM("v_mfma_f32_16x16x32_bf16");
-#undef LORA_MFMA4_ASM
-}
-
+// TILE: inside a tile kernel.
 template <int IN, bool TILE, int NC>
-__device__ __forceinline__ void lora_mac(const v4i (&b)[NC], const LoraV& V, v4f (&y)[NC]) {
+__device__ __forceinline__ void lora_mac(const v4i (&b)[NC], const LoraV<IN>& V, v4f (&y)[NC]) {
     static_assert(!TILE || NC == 4, "four channel blocks");
     v4f t[NC];
 #pragma unroll
     for (int c = 0; c < NC; ++c) t[c] = IN == 2 ? y[c] : v4f{0, 0, 0, 0};
-    if constexpr (TILE) {
-        lora_mfma4_asm<IN>(b, V, t);
+    if constexpr (IN == 2 && TILE) {
+        lora_mfma4_bf16(b, V.part, t);
     } else {
 #pragma unroll
-        for (int c = 0; c < NC; ++c) t[c] = lora_mfma<IN>(b[c], V.lo, t[c]);
+        for (int p = 0; p < LoraV<IN>::PARTS; ++p) {
+            if constexpr (TILE) {
+                lora_mfma4_f16(b, V.part[p], t);
+            } else {
 #pragma unroll
-        for (int c = 0; c < NC; ++c) t[c] = lora_mfma<IN>(b[c], V.hi, t[c]);
+                for (int c = 0; c < NC; ++c) t[c] = lora_mfma<IN>(b[c], V.part[p], t[c]);
+            }
+            if (IN == 1 && p == 0)
+#pragma unroll
+                for (int c = 0; c < NC; ++c)
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) t[c][q] *= 1.0f / kLoraLow;
+        }
     }
 #pragma unroll
     for (int c = 0; c < NC; ++c)
@@ -175,7 +204,7 @@ __device__ __forceinline__ void lora_add(const LoraArgs& L, int id, int N, int n
     const unsigned any = (unsigned)__ballot(id >= 0) & 0xFFFFu;
     if (any == 0) return;
     for (int s = 0; 32 * s < L.R; ++s) {
-        const LoraV V = get_v(s);
+        const LoraV<IN> V = get_v(s);
         unsigned rest = any;
         while (rest) {
             int a[BATCH];
