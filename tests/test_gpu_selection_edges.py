@@ -122,3 +122,76 @@ def test_lora_inner_product_is_kept_in_float32(M, N, K, R, dt):
         want[m] = V[m] @ B[a].T
         size[m] = np.abs(V[m]) @ np.abs(B[a]).T
     within(got, want, 8 * ref.U * size + ref.rounding(want, "f16"))
+
+
+@pytest.mark.parametrize("dt", ["f16", "bf16"])
+@pytest.mark.parametrize("M,N,K,R", PATHS)
+def test_lora_infinities(M, N, K, R, dt):
+    """Infinite elements of B (and of A) give the infinity, or the NaN, that
+    the products of the definition give: a positive or negative infinity
+    where the infinite terms agree, NaN where they do not or where the inner
+    product is zero; in the rows of that adapter only."""
+    say(f"lora inf M={M} N={N} K={K} R={R} {dt}")
+    n = 4
+    inf = float("inf")
+    p, rng, ad, X, A, B = bare(M, N, K, R, n, dt, M + R + 1)
+    ad[:5] = [0, 1, 2, 3, -1]
+    eight = rng.integers(128, 256, (M, 2)) / 128.0
+    X[:, 0] = eight[:, 0] * rng.choice([-1, 1], M)
+    X[:, 1] = eight[:, 1] * 2.0 ** -8
+    X[:, 2] = 1.0
+    if M > 64:
+        X[M // 2] = 0.0          # inner products of exactly 0
+    A[:, :, 0] = rng.choice([-1, 1], (n, R))
+    A[:, :, 1] = 1.0
+    A[1, :, 1] = 0.0             # 8 significant bits: nothing behind the first part
+    A[0, R - 1, 2] = 2.0 ** 14   # next to it the others are small ...
+    A[0, R - 2] = 0.0
+    A[0, R - 2, 2] = 2.0 ** -14  # ... and this one tiny
+    A[3, 2, 2] = inf             # an infinite inner product
+    B[:] = rng.choice([-1, 1], (n, N, R)) * 2.0 ** -10
+    B[0, 3::7, R - 2] = -inf
+    B[0, 4::7, 1] = inf
+    B[1, 5::7, 0] = inf
+    B[1, 6::7, 0] = inf
+    B[1, 6::7, 3] = -inf
+    B[2, ::5, R - 1] = -inf
+    B[3, ::3, 2] = 0.0
+    got = adapters(p, X, A, B, ad, dt)
+    want, size = np.zeros((M, N)), np.zeros((M, N))
+    with np.errstate(invalid="ignore"):
+        for a in range(n):
+            m = ad == a
+            # (a column of A that is infinite: 0 x inf only where X is 0)
+            V = np.where(X[m][:, None, :] == 0, np.where(np.isinf(A[a])[None], np.nan, 0.0),
+                         X[m][:, None, :] * A[a][None]).sum(2)
+            for c0 in range(0, N, 256):
+                c = slice(c0, min(N, c0 + 256))
+                terms = V[:, None, :] * B[a, c][None]
+                want[m, c] = terms.sum(2)
+                size[m, c] = np.abs(terms).sum(2)
+    for f in (np.isnan, np.isposinf, np.isneginf):
+        bad = f(got) != f(want)
+        assert not bad.any(), (f.__name__, int(bad.sum()), np.argwhere(bad)[:5], got[bad][:5],
+                               want[bad][:5])
+    ok = np.isfinite(want)
+    # V of at most 24 + 14 bits: two float32 sums of R and a few terms
+    within(got[ok], want[ok], (2 * R + 12) * ref.U * size[ok] + ref.rounding(want[ok], "f16"))
+
+
+def test_lora_largest_inner_product():
+    """An inner product next to float32's largest value, whose first part of
+    bfloat16 rounds to an infinity, times a tiny B."""
+    M, N, K, R = 6, 128, 256, 8
+    p, rng, ad, X, A, B = bare(M, N, K, R, 2, "bf16", 3)
+    ad[:] = [0, 1, -1, 0, 1, 1]
+    X[:, :3] = [1.0, 2.0 ** -8, 2.0 ** -16]
+    A[:, 3, :3] = 255 / 128 * 2.0 ** 127   # 24 ones: float32's largest
+    A[1] *= -1
+    B[:, :, 3] = 2.0 ** -120
+    B[:, ::2, 5] = float("inf")            # (times an inner product of 0)
+    got = adapters(p, X, A, B, ad, "bf16")
+    want = np.zeros((M, N))
+    want[ad == 0], want[ad == 1] = 256.0, -256.0   # (2^128 - 2^104) 2^-120 in fp16
+    want[ad >= 0, ::2] = np.nan
+    within(got, want, 0.0)

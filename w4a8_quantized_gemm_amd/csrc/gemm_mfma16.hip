@@ -219,6 +219,25 @@ __device__ __forceinline__ void read_blocks(const v4i (&acc)[RB][4], int rb, v4i
     }
 }
 
+// One channel block of row block rb (uniform), likewise.
+template <int LO, int HI, int RB>
+__device__ __forceinline__ v4i read_quad(const v4i (&acc)[RB][4], int rb, int cb) {
+    if constexpr (HI - LO == 1) {
+        v4i cur;
+#pragma unroll
+        for (int v = 0; v < 4; ++v) {
+            int x;
+            asm volatile("v_accvgpr_read_b32 %0, %1" : "=v"(x) : "a"(acc[LO][cb][v]));
+            cur[v] = x;
+        }
+        return cur;
+    } else {
+        constexpr int MID = (LO + HI) / 2;
+        if (rb < MID) return read_quad<LO, MID>(acc, rb, cb);
+        return read_quad<MID, HI>(acc, rb, cb);
+    }
+}
+
 // Epilogue with low-rank adapters.  Accumulator layout as in the kernel's own
 // epilogue.  Row blocks are walked in a loop that is not unrolled, with a
 // uniform choice of the block's accumulators in front (their registers have
@@ -247,6 +266,7 @@ __device__ __forceinline__ void mfma16_lora_epilogue(v4i (&acc)[MT / 16][4], uin
     uint8_t* stage = lds + wave * (16 * PB * RSTR);
     unsigned short* yp = Y + (size_t)(m0 + (lane >> 3)) * N + n0 + (lane & 7) * 8;
     LoraHeld<MT == 256 ? 4 : 1> held;
+    uint64_t nan = 0;  // lanes that held one
 #pragma clang loop unroll(disable)
     for (int rb = 0; rb < MT / 16; rb += PB) {
         v4i cur[PB][4];
@@ -293,6 +313,8 @@ __device__ __forceinline__ void mfma16_lora_epilogue(v4i (&acc)[MT / 16][4], uin
                 held, y[p]);
         }
 #pragma unroll
+        for (int p = 0; p < PB; ++p) nan |= lora_nan(id[p], y[p]);
+#pragma unroll
         for (int p = 0; p < PB; ++p)
 #pragma unroll
             for (int cb = 0; cb < 4; ++cb) {
@@ -317,6 +339,47 @@ __device__ __forceinline__ void mfma16_lora_epilogue(v4i (&acc)[MT / 16][4], uin
         yp += (size_t)(16 * PB) * N;
         asm volatile("" ::: "memory");
         __builtin_amdgcn_wave_barrier();
+    }
+    if (__builtin_expect(nan == 0, 1)) return;
+    // the results that came out as NaN again, from Y as just written (inside
+    // the loop above this would cost registers that it does not have)
+    __threadfence();
+#pragma clang loop unroll(disable)
+    for (int rb = 0; rb < MT / 16; ++rb) {
+        const int row = 16 * rb + r, id = pre.ids[row];
+        unsigned short* out = Y + (size_t)(m0 + row) * N + n0 + 4 * G;
+        v4f y[4];
+#pragma unroll
+        for (int cb = 0; cb < 4; ++cb) {
+            uint2 h{0, 0};
+            if (id >= 0) h = *reinterpret_cast<const uint2*>(out + 16 * cb);
+#pragma unroll
+            for (int v = 0; v < 4; ++v)
+                y[cb][v] = (float)__builtin_bit_cast(
+                    _Float16, (unsigned short)((v < 2 ? h.x : h.y) >> (16 * (v & 1))));
+        }
+        if (lora_nan(id, y) == 0) continue;
+        lora_redo<LORA>(
+            lora, id, m0 + row, N, n0,
+            [&](int cb) {
+                const v4i sum = read_quad<0, MT / 16>(acc, rb, cb);
+                const v4f w =
+                    *reinterpret_cast<const v4f*>(&pre.sw[wave * kColsPerWave + 16 * cb + 4 * G]);
+                v4f s;
+#pragma unroll
+                for (int v = 0; v < 4; ++v) s[v] = ((float)sum[v] * pre.sx[row]) * w[v];
+                return s;
+            },
+            y);
+        if (id < 0) continue;
+#pragma unroll
+        for (int cb = 0; cb < 4; ++cb) {
+            unsigned short h[4];
+#pragma unroll
+            for (int v = 0; v < 4; ++v) h[v] = f32_to_f16_bits(y[cb][v]);
+            *reinterpret_cast<uint2*>(out + 16 * cb) =
+                uint2{h[0] | ((unsigned)h[1] << 16), h[2] | ((unsigned)h[3] << 16)};
+        }
     }
 }
 

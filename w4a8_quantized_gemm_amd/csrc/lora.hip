@@ -258,11 +258,15 @@ __global__ __launch_bounds__(256) void lora_join_kernel(const int* __restrict__ 
             for (int c = 0; c < 4; ++c)
                 sum[c] += load16(acc + ((size_t)p * M + m) * N + n0 + 16 * c + 4 * G);
     const float s = live ? sx[m] : 0.0f;
+    auto scaled = [&](int c) {
+        v4f o;
+#pragma unroll
+        for (int v = 0; v < 4; ++v) o[v] = ((float)sum[c][v] * s) * sw[n0 + 16 * c + 4 * G + v];
+        return o;
+    };
     v4f y[4];
 #pragma unroll
-    for (int c = 0; c < 4; ++c)
-#pragma unroll
-        for (int v = 0; v < 4; ++v) y[c][v] = ((float)sum[c][v] * s) * sw[n0 + 16 * c + 4 * G + v];
+    for (int c = 0; c < 4; ++c) y[c] = scaled(c);
     lora_add<IN, false>(
         L, id, N, n0,
         [&](int p) {
@@ -271,6 +275,7 @@ __global__ __launch_bounds__(256) void lora_join_kernel(const int* __restrict__ 
             return lora_split<IN>(v);
         },
         y);
+    lora_redo<IN>(L, id, m, N, n0, scaled, y);
     if (!live) return;
 #pragma unroll
     for (int c = 0; c < 4; ++c) {

@@ -269,4 +269,63 @@ __device__ __forceinline__ void lora_add_held(const LoraArgs& L, int id, int N, 
     }
 }
 
+// Lanes with a NaN among the results of a row that has an adapter.
+template <int NC>
+__device__ __forceinline__ uint64_t lora_nan(int id, const v4f (&y)[NC]) {
+    bool nan = false;
+#pragma unroll
+    for (int c = 0; c < NC; ++c)
+        nan |= __builtin_isunordered(y[c][0], y[c][1]) || __builtin_isunordered(y[c][2], y[c][3]);
+    return __ballot(nan && id >= 0);
+}
+
+// Results that came out as NaN are formed again, y = base + V . B in plain
+// float32: an infinite element of B meets parts of V of both signs or of
+// zero, and V may lie beyond its first part's range, where the definition
+// gives an infinity or a number.  Called once behind the adapters' products of
+// a block (y, id, m, n0 as in lora_add); base(c) gives its scaled sums.  The
+// branch is not taken for finite operands.
+template <int IN, int NC, typename Base>
+__device__ __forceinline__ void lora_redo(const LoraArgs& L, int id, int m, int N, int n0,
+                                          Base base, v4f (&y)[NC]) {
+    if (__builtin_expect(lora_nan(id, y) == 0, 1)) return;
+    unsigned redo = 0;  // bit 4 c + q
+#pragma unroll
+    for (int c = 0; c < NC; ++c) {
+        const v4f s = base(c);
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+            if (id >= 0 && y[c][q] != y[c][q]) {
+                redo |= 1u << (4 * c + q);
+                y[c][q] = s[q];
+            }
+    }
+    const int G = (threadIdx.x & 63) >> 4;
+#pragma clang loop unroll(disable)
+    for (int k = 0; k < 4 * NC; ++k) {
+        float sum = 0.0f;
+        if ((redo >> k) & 1) {
+            const size_t row = (size_t)id * N + n0 + 16 * (k >> 2) + 4 * G + (k & 3);
+            const uint8_t* w = reinterpret_cast<const uint8_t*>(L.B) + row * L.R * 2;
+            const float* v = L.V + (size_t)m * L.R;
+#pragma clang loop unroll(disable)
+            for (int r = 0; r < L.R; r += 8) {
+                const v4i b = load16(w + 2 * r);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const unsigned h = ((unsigned)b[j >> 1] >> (16 * (j & 1))) & 0xFFFFu;
+                    const float x = IN == 1 ? (float)__builtin_bit_cast(_Float16, (unsigned short)h)
+                                            : __builtin_bit_cast(float, h << 16);
+                    sum = fmaf(v[r + j], x, sum);
+                }
+            }
+        }
+#pragma unroll
+        for (int c = 0; c < NC; ++c)
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+                if (k == 4 * c + q && ((redo >> k) & 1)) y[c][q] += sum;
+    }
+}
+
 }  // namespace w4a8

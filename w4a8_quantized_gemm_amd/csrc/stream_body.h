@@ -340,9 +340,13 @@ __device__ __forceinline__ void stream_body(
             for (int w = 0; w < ks; ++w)
                 sum += *reinterpret_cast<const v4i*>(
                     &red[((w * RB + rb) * NTW + t) * 256 + (r & 3) * 64 + 16 * (r >> 2) + 4 * G]);
-            v4f y[1];
+            auto scaled = [&](int) {
+                v4f s;
 #pragma unroll
-            for (int q = 0; q < 4; ++q) y[0][q] = ((float)sum[q] * xs) * ws[q];
+                for (int q = 0; q < 4; ++q) s[q] = ((float)sum[q] * xs) * ws[q];
+                return s;
+            };
+            v4f y[1] = {scaled(0)};
             lora_add<LORA, false>(
                 lora, id, N, n,
                 [&](int s) {
@@ -351,6 +355,7 @@ __device__ __forceinline__ void stream_body(
                     return lora_split<LORA>(v);
                 },
                 y);
+            lora_redo<LORA>(lora, id, m, N, n, scaled, y);
             if (!live) continue;
             unsigned short h[4];
 #pragma unroll
