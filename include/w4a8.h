@@ -34,6 +34,10 @@
  *     group in {64, 128}.  For every GEMM: M*K < 2^31 and N*K < 2^32 (the
  *     kernels address operands with 32-bit buffer ranges); larger problems
  *     return W4A8_ERR_SHAPE (split M across calls).
+ *   - An int32 sum of INT8 products is exact whatever the codes for K up to
+ *     W4A8_EXACT_MAX_K (127 * 128 * 131072 < 2^31).  The GEMMs also take
+ *     longer rows, whose sums are exact while they lie within int32;
+ *     w4a8_moe and w4a8_gemm_lora do not.
  *   - Alignment (W4A8_ERR_ALIGNMENT otherwise): the byte and element
  *     arrays -- W, X, Xq, wq, wq8, s_u8, a_u8, Y and any workspace -- start
  *     on a 16-byte boundary (the kernels move them in 16-byte pieces); the
@@ -80,6 +84,7 @@ typedef enum {
 } w4a8_status_t;
 
 #define W4A8_LAYOUT_VERSION 1
+#define W4A8_EXACT_MAX_K 131072
 
 enum { W4A8_PACK_LQQ = 0, W4A8_PACK_INT4_SYM = 1 };
 enum { W4A8_OUT_F16 = 0, W4A8_OUT_I32 = 1 };
@@ -428,7 +433,7 @@ w4a8_status_t w4a8_route(const void* logits, int in_type, int T, int E, int k,
  *   out_type (W4A8_IN_*).  A slot of weight 0 adds nothing, a token without
  *   an expert gives zeros.  A token with an element that is not finite, or
  *   whose h overflows float32, gives NaN (other tokens are unaffected).
- * H % 128 = 0, F % 128 = 0, both < 2^19, 2 F H < 2^32; 1 <= E <=
+ * H % 128 = 0, F % 128 = 0, both <= W4A8_EXACT_MAX_K, 2 F H < 2^32; 1 <= E <=
  * W4A8_MAX_EXPERTS, 1 <= k <= W4A8_MAX_TOPK.  X, Y and the byte arrays
  * 16-byte aligned, the others 4-byte.  workspace: w4a8_moe_workspace_size
  * bytes, 16-byte aligned, contents ignored and undefined afterwards.
@@ -458,9 +463,10 @@ w4a8_status_t w4a8_moe(const void* X, int in_type, const int32_t* ids,
  *     smaller rank are padded with zero rows of A (or columns of B).
  *   wq, s_u8, a_u8, sw: w4a8_pack (LQQ) of the shared weights.
  * R a multiple of 8, 8 <= R <= W4A8_LORA_MAX_RANK; n_adapters = 0 is
- * w4a8_gemm (A, B, scale unread).  Sizes as w4a8_gemm.  X, A, B, Y and the
- * byte arrays 16-byte aligned, the others 4-byte.  workspace:
- * w4a8_gemm_lora_workspace_size bytes, 16-byte aligned.
+ * w4a8_gemm (A, B, scale unread).  Sizes as w4a8_gemm, K at most
+ * W4A8_EXACT_MAX_K.  X, A, B, Y and the byte arrays 16-byte aligned, the
+ * others 4-byte.  workspace: w4a8_gemm_lora_workspace_size bytes, 16-byte
+ * aligned.
  */
 size_t w4a8_gemm_lora_workspace_size(int M, int N, int K, int R);
 w4a8_status_t w4a8_gemm_lora(const void* X, int in_type, const uint8_t* wq,

@@ -195,3 +195,31 @@ def test_lora_largest_inner_product():
     want[ad == 0], want[ad == 1] = 256.0, -256.0   # (2^128 - 2^104) 2^-120 in fp16
     want[ad >= 0, ::2] = np.nan
     within(got, want, 0.0)
+
+
+@pytest.mark.parametrize("T", [1, 3])
+@pytest.mark.parametrize("H,F", [(w4.EXACT_MAX_K, 128), (128, w4.EXACT_MAX_K)])
+def test_moe_longest_rows(T, H, F):
+    """The longest rows with the largest codes: int32 sums 1.6 % below the
+    wrap."""
+    say(f"moe longest T={T} H={H} F={F}")
+    g = 128
+    up, down = 0.7 / H, 0.3 / F
+    w13 = w4.pack_experts(torch.full((1, 2 * F, H), up, device=DEV), group=g)
+    w2 = w4.pack_experts(torch.full((1, H, F), down, device=DEV), group=g)
+    W13, W2 = np.full((1, 2 * F, H), 127, np.int8), np.full((1, H, F), 127, np.int8)
+    for p, W in ((w13, W13), (w2, W2)):
+        part = slice(0, 64 * W.shape[2] // 2)
+        np.testing.assert_array_equal(
+            ref.decode_weights(p["wq"][part].cpu().numpy(),
+                               p["s_u8"][:64 * W.shape[2] // g].cpu().numpy(),
+                               p["a_u8"][:64 * W.shape[2] // g].cpu().numpy(), 64, W.shape[2], g),
+            W[0, :64])
+    X = torch.ones((T, H), dtype=torch.float16, device=DEV)
+    ids, w = np.zeros((T, 1), np.int32), np.full((T, 1), 1.5, np.float32)
+    Y = poison((T, H), torch.float32)
+    w4.moe(X, torch.from_numpy(ids).to(DEV), torch.from_numpy(w).to(DEV), w13, w2, out=Y)
+    one = slice(0, 1)  # every token is the same
+    want, tol = ref.moe(X[one].float().cpu().numpy(), ids[one], w[one], W13,
+                        w13["sw"].cpu().numpy()[None], W2, w2["sw"].cpu().numpy()[None], "f32")
+    within(f64(Y), np.repeat(want, T, 0), np.repeat(tol, T, 0))

@@ -41,6 +41,7 @@ IN_F32, IN_F16, IN_BF16 = 0, 1, 2
 ABL_LQQ, ABL_AFFINE16, ABL_LQQ_COARSE = 0, 1, 2
 LAYOUT_VERSION = 1
 MAX_EXPERTS, MAX_TOPK, MOE_MAX_TOKENS, LORA_MAX_RANK = 512, 16, 256, 128
+EXACT_MAX_K = 131072
 
 EXPORTS = ("w4a8_pack", "w4a8_quant_act", "w4fp8_quant_act",
            "w4a8_quant_act_ex", "w4fp8_quant_act_ex", "w4a8_workspace_size", "w4a8_gemm",

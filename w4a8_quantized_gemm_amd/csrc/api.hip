@@ -146,13 +146,17 @@ bool valid_route(int T, int E, int k) {
            (long long)T * E < (1LL << 31);
 }
 
+// Longest sum of products of INT8 codes (|x| <= 127, |w| <= 128) that int32
+// holds whatever the codes: 127 * 128 * 131072 < 2^31.
+bool exact_sum(int K) { return K <= W4A8_EXACT_MAX_K; }
+
 // The layer for a few tokens: rows of W13 [2F][H] and W2 [H][F] per expert
 // within a GEMM's limits (k <= E is the router's concern: a caller may give
 // any ids).
 bool valid_moe(int T, int E, int k, int H, int F) {
     return T >= 0 && T <= W4A8_MOE_MAX_TOKENS && E >= 1 && E <= W4A8_MAX_EXPERTS && k >= 1 &&
            k <= W4A8_MAX_TOPK && H > 0 && H % 128 == 0 && F > 0 && F % 128 == 0 &&
-           H < (1 << 19) && F < (1 << 19) && 2LL * F * H < (1LL << 32);
+           exact_sum(H) && exact_sum(F) && 2LL * F * H < (1LL << 32);
 }
 
 bool valid_rank(int R) { return R >= 8 && R <= W4A8_LORA_MAX_RANK && R % 8 == 0; }
@@ -598,7 +602,9 @@ struct LoraLayout {
 }  // namespace
 
 W4A8_EXPORT size_t w4a8_gemm_lora_workspace_size(int M, int N, int K, int R) {
-    if (M <= 0 || N == 0 || !valid_nk(N, K) || !valid_extent(M, N, K) || !valid_rank(R)) return 0;
+    if (M <= 0 || N == 0 || !valid_nk(N, K) || !valid_extent(M, N, K) || !valid_rank(R) ||
+        !exact_sum(K))
+        return 0;
     return LoraLayout(M, N, K, R).bytes;
 }
 
@@ -612,7 +618,7 @@ W4A8_EXPORT w4a8_status_t w4a8_gemm_lora(const void* X, int in_type, const uint8
     if (in_type != W4A8_IN_F16 && in_type != W4A8_IN_BF16) return W4A8_ERR_UNSUPPORTED;
     if (M < 0 || !valid_nk(N, K) || !valid_group(group) || !valid_rank(R) || n_adapters < 0)
         return W4A8_ERR_SHAPE;
-    if (!valid_extent(M, N, K)) return W4A8_ERR_SHAPE;
+    if (!valid_extent(M, N, K) || !exact_sum(K)) return W4A8_ERR_SHAPE;
     if (M == 0 || N == 0) return W4A8_OK;  // nothing to read or write
     if (!X || !wq || !s_u8 || !a_u8 || !sw || !adapter || !Y) return W4A8_ERR_NULL_PTR;
     if (n_adapters > 0 && (!A || !B || !scale)) return W4A8_ERR_NULL_PTR;
