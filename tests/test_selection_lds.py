@@ -1,5 +1,5 @@
-"""LDS reuse in the expert layer's kernels, checked in this build's own gfx950
-assembly (CPU only).
+"""LDS use of the expert layer's and the adapters' kernels (CPU only), mostly
+checked in this build's own gfx950 assembly.
 
 moe_product_kernel keeps the X tiles of its waves and, behind them in time,
 the partial sums of all waves in the same LDS bytes, and walks the rows of an
@@ -10,10 +10,11 @@ write of an X tile (16-byte LDS writes) there is a barrier.
 """
 import os
 import re
+import subprocess
 
 import pytest
 
-from test_isa_hazards import HIPCC, _asm, _blocks, _functions
+from test_isa_hazards import CSRC, HIPCC, ROOT, _asm, _blocks, _functions
 
 
 @pytest.fixture(scope="module")
@@ -59,3 +60,22 @@ def test_sums_are_read_before_the_next_rows_tiles(kernels):
         assert any(m.endswith("b128") and m.startswith("ds_write") for m in mnemonics), name
         assert any(re.fullmatch(r"ds_read(2|2st64)?_b32", m) for m in mnemonics), name
         assert unordered(items) == 0, name
+
+
+def test_adapter_epilogue_lds_is_aligned(tmp_path):
+    """The tile kernels' epilogue with adapters reads and writes LDS in pieces
+    of 16 bytes: its object, and the arrays in it, are declared so."""
+    if not os.path.exists(HIPCC):
+        pytest.skip("hipcc not available")
+    src = tmp_path / "aligned.hip"
+    src.write_text('#include "gemm_mfma16.hip"\n#include <cstddef>\n' + "".join(
+        f"using L{mt}_{t} = w4a8::LoraLds<{mt}, {t}>;\n"
+        f"static_assert(alignof(L{mt}_{t}) % 16 == 0, \"object\");\n"
+        f"static_assert(offsetof(L{mt}_{t}, v) % 16 == 0, \"operands\");\n"
+        f"static_assert(offsetof(L{mt}_{t}, sw) % 16 == 0, \"scales\");\n"
+        for mt in (128, 256) for t in (1, 2)))
+    res = subprocess.run(
+        [HIPCC, "--offload-arch=gfx950", "-std=c++17", "--offload-device-only", "-fsyntax-only",
+         "-I", os.path.join(ROOT, "include"), "-I", CSRC, str(src)],
+        capture_output=True, text=True)
+    assert res.returncode == 0, res.stderr

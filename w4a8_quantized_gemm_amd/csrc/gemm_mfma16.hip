@@ -165,10 +165,11 @@ __device__ __forceinline__ void mfma16_drain(v4i (&acc)[RB][4]) {
 template <int LORA>
 constexpr unsigned kLoraVStride = 4 * LoraV<LORA>::PARTS * 16 + 16;
 template <int MT, int LORA>
-struct LoraLds {
-    uint8_t v[MT * kLoraVStride<LORA>];
+struct alignas(16) LoraLds {  // (v and sw are read 16 bytes at a time)
+    alignas(16) uint8_t v[MT * kLoraVStride<LORA>];
+    alignas(16) float sw[kNT];
     float backs[LORA == 1 ? MT * 4 : 4];  // [32 ranks][row]
-    float sx[MT], sw[kNT];
+    float sx[MT];
     int ids[MT];
 };
 
