@@ -347,7 +347,7 @@ RoutePlan plan_route(int T, int E, int k) {
         return p;
     }
     p.tokens = T <= 2048 ? 16 : 32 * (int)((T + 32LL * 512 - 1) / (32 * 512));
-    p.blocks = (T + p.tokens - 1) / p.tokens;
+    p.blocks = (int)(((long long)T + p.tokens - 1) / p.tokens);
     p.workspace = (size_t)p.blocks * E * sizeof(int);
     return p;
 }
