@@ -175,21 +175,25 @@ __device__ __forceinline__ int channel_group(int b, int n) {
     return (n & 7) ? b : (b & 7) * (n >> 3) + (b >> 3);
 }
 
-// One product of the layer for one expert and 16 NT channels of each half:
+// 16-channel tiles of each half per workgroup of the products (half a panel of
+// group parameters).
+constexpr int kMoeTiles = 2;
+
+// One product of the layer for one expert and 32 channels of each half:
 // HALVES = 2: the gate and up products of W13 (channel n and F + n), h = silu;
 // HALVES = 1: the down product, scaled by the slot's weight, into part[slot].
 // blockIdx.x: channel group, blockIdx.y: index into the active experts.  The
 // `ks` waves take interleaved K-tiles and are summed in LDS (exact int32).
 // Up to 16 RB rows share each decoded weight; the rows of an expert with more
 // are dealt to the workgroups of blockIdx.z, and past those repeat the stream.
-template <int HALVES, int NT, int RB, int D, int GROUP>
+template <int HALVES, int RB, int D, int GROUP>
 __global__ __launch_bounds__(512) void moe_product_kernel(
     const int8_t* __restrict__ Xq, const float* __restrict__ sx, const uint8_t* __restrict__ wq,
     const uint8_t* __restrict__ s_u8, const uint8_t* __restrict__ a_u8,
     const float* __restrict__ sw, const float* __restrict__ weights,
     const MoeHead* __restrict__ head, const int* __restrict__ slots, float* __restrict__ out,
     int N, int K, int k, int rows_in) {
-    constexpr int TT = HALVES * NT;  // weight tiles of the workgroup
+    constexpr int NT = kMoeTiles, TT = HALVES * NT;  // weight tiles of the workgroup
     extern __shared__ int red[];
     if ((int)blockIdx.y >= head->active) return;
     const MoeActive act = head->list[blockIdx.y];
@@ -280,7 +284,7 @@ __global__ __launch_bounds__(512) void moe_product_kernel(
             }
 #pragma unroll
             for (int t = 0; t < TT; ++t) {
-                const int b = (NT == 4 ? t % NT : (nt0 & 3) + t % NT);
+                const int b = (nt0 & 3) + t % NT;
                 const u16x2 s2 = scale_pair(S.s[t / NT], b), a4 = offset_quad(S.a[t / NT], b);
                 unsigned q[8];
                 lqq_dequant8((unsigned)S.w[t].x, s2, a4, q[0], q[1]);
@@ -468,7 +472,7 @@ __global__ __launch_bounds__(256, 4) void moe_few_kernel(
     const uint8_t* __restrict__ wq, const uint8_t* __restrict__ s_u8,
     const uint8_t* __restrict__ a_u8, const float* __restrict__ sw, float* __restrict__ out, int S,
     int E, int k, int N, int K, int cap) {
-    constexpr int NT = 2, TT = HALVES * NT, D = HALVES == 2 ? 2 : 4, WAVES = 4;
+    constexpr int NT = kMoeTiles, TT = HALVES * NT, D = HALVES == 2 ? 2 : 4, WAVES = 4;
     extern __shared__ __attribute__((aligned(16))) uint8_t few_lds[];
     uint8_t* const lds = few_lds;
     __shared__ float scales[16];
@@ -814,14 +818,14 @@ int row_sharers(int T, int rb) {
     return all < 4 ? all : 4;
 }
 
-// Two tiles of each half per workgroup.  Waves splitting K: four, eight for
+// Waves splitting K: four, eight for
 // the down product of wide experts (14336 x 4096, one token: the layer in
 // 47.5 us against 50.5).
 template <int HALVES, int RB, int D>
 void launch_product(const int8_t* xq, const float* sx, const MoeWeights& w, const float* weights,
                     const MoeHead* head, const int* slots, float* out, int N, int K, int k,
                     int rows_in, int experts, int group, int sharers, hipStream_t st) {
-    constexpr int NT = 2;
+    constexpr int NT = kMoeTiles;
     const int ks = HALVES == 1 && RB == 1 && K >= 64 * kTileK ? 8 : 4;
     const dim3 grid(N / HALVES / (kTileN * NT), experts, sharers), block(64 * ks);
     // X slots, then the sums of one row block
@@ -829,11 +833,11 @@ void launch_product(const int8_t* xq, const float* sx, const MoeWeights& w, cons
     const size_t rbytes = (size_t)ks * HALVES * NT * 256 * sizeof(int);
     const size_t lds = xbytes > rbytes ? xbytes : rbytes;
     if (group == 64)
-        hipLaunchKernelGGL((moe_product_kernel<HALVES, NT, RB, D, 64>), grid, block, lds, st, xq,
+        hipLaunchKernelGGL((moe_product_kernel<HALVES, RB, D, 64>), grid, block, lds, st, xq,
                            sx, w.wq, w.s_u8, w.a_u8, w.sw, weights, head, slots, out, N, K, k,
                            rows_in);
     else
-        hipLaunchKernelGGL((moe_product_kernel<HALVES, NT, RB, D, 128>), grid, block, lds, st, xq,
+        hipLaunchKernelGGL((moe_product_kernel<HALVES, RB, D, 128>), grid, block, lds, st, xq,
                            sx, w.wq, w.s_u8, w.a_u8, w.sw, weights, head, slots, out, N, K, k,
                            rows_in);
 }
@@ -844,8 +848,8 @@ size_t few_rows_lds(int rows, int K) { return 16 + (size_t)rows * (K + 16); }
 template <int HALVES, int IN, int GROUP>
 void launch_few_type(const void* X, const int* ids, const float* weights, const MoeWeights& w,
                      float* out, int S, int E, int k, int N, int K, int cap, hipStream_t st) {
-    const dim3 grid(N / HALVES / 32, E < S ? E : S);
-    const size_t red = (size_t)4 * HALVES * 2 * 256 * sizeof(int);  // the sums, over the rows
+    const dim3 grid(N / HALVES / (kTileN * kMoeTiles), E < S ? E : S);
+    const size_t red = (size_t)4 * HALVES * kMoeTiles * 256 * sizeof(int);  // the sums, over the rows
     const size_t lds = few_rows_lds(cap, K);
     hipLaunchKernelGGL((moe_few_kernel<HALVES, IN, GROUP>), grid, dim3(256), lds > red ? lds : red,
                        st, X, ids, weights, w.wq, w.s_u8, w.a_u8, w.sw, out, S, E, k, N, K, cap);
