@@ -223,3 +223,25 @@ def test_moe_longest_rows(T, H, F):
     want, tol = ref.moe(X[one].float().cpu().numpy(), ids[one], w[one], W13,
                         w13["sw"].cpu().numpy()[None], W2, w2["sw"].cpu().numpy()[None], "f32")
     within(f64(Y), np.repeat(want, T, 0), np.repeat(tol, T, 0))
+
+
+# ------------------------------------------------------------------ route ---
+@pytest.mark.parametrize("T,E,k", [(2 ** 31 - 1, 1, 1), ((2 ** 31 - 1) // 3, 3, 2)])
+def test_route_largest_batches(T, E, k):
+    """T * E next to 2^31: outputs past 4 GiB, slots up to 2^31 - 2."""
+    say(f"route largest T={T} E={E} k={k}")
+    x = torch.zeros((T, E), dtype=torch.bfloat16, device=DEV)
+    x[T // 2, E - 1] = 1.0
+    x[T - 1] = float("-inf")
+    r = w4.route(x, k)
+    offsets, ids, rows = r["offsets"].tolist(), r["ids"], r["rows"]
+    # ties: the first k experts, but for one token, and the last has none
+    assert offsets[0] == 0 and offsets[E] == (T - 1) * k
+    assert ids[T // 2, 0].item() == E - 1 and (ids[T - 1] == -1).all()
+    assert (rows[(T - 1) * k:] == -1).all()
+    for e in range(E):
+        for lo in range(offsets[e], offsets[e + 1], 1 << 26):
+            part = rows[lo:min(offsets[e + 1], lo + (1 << 26))].long()
+            assert (part[1:] > part[:-1]).all() and (ids.view(-1)[part] == e).all()
+    del x, r, ids, rows
+    torch.cuda.empty_cache()
