@@ -8,8 +8,9 @@
 // shared projection alone.
 //
 // This file: the inner product V = scale (X . A^T), with the quantisation of
-// X in the same launch for small calls, and the epilogue of projections
-// whose int32 sums (one or several K parts) lie in memory.
+// X in the same launch (except for rows longer than its kernels hold in
+// registers: K above 32768, 16384 from 512 rows on), and the epilogue of
+// projections whose int32 sums (one or several K parts) lie in memory.
 #include "act_common.h"
 #include "launch.h"
 #include "lora_common.h"

@@ -5,9 +5,9 @@
 // instruction per 32 ranks and operand part.  B is used as stored (fp16 or
 // bfloat16, 16 bytes per lane straight from memory); V is float32 and is
 // split into operands of B's type, each rounded to nearest:
-//   bfloat16: three parts of 8 bits, V exactly (two, 16 bits of V, took 754 us
-//     against 760 at 4096 x 28672 x 8192, rank 16, and 22.9 against 23.4 at
-//     47 x 11008 x 4096, rank 64);
+//   bfloat16: three parts of 8 bits, V exactly from 2^-100 on (two, 16 bits,
+//     took 754 us against 760 at 4096 x 28672 x 8192, rank 16, and 22.9
+//     against 23.4 at 47 x 11008 x 4096, rank 64);
 //   fp16: the 32 ranks of a row are first scaled by a power of two that
 //     brings their largest to [2^14, 2^15) (V's range is not fp16's), then
 //     split into two parts, the second times 2^11 so that it keeps its bits
@@ -236,7 +236,12 @@ __device__ __forceinline__ void lora_add(const LoraArgs& L, int id, int N, int n
 }
 
 // B operands of one adapter held in registers over consecutive row blocks,
-// for adapters of at most 32 NS ranks.
+// for adapters of at most 32 NS ranks: 128 of them in the 256-row tile kernel,
+// 32 in the 128-row one, which spills 21 registers with 64.  Held against
+// loaded again for every block, us: 4096 x 28672 x 8192 (256 rows) rank 16
+// 800 / 815, 64 894 / 952, 128 1122 / 1257; 2048 x 4096 x 4096 (128 rows)
+// rank 16 51.1 / 51.5, 32 56.5 / 56.9, and beyond 32 ranks, where both load,
+// 40 69 / 68, 128 125 / 124.
 template <int NS>
 struct LoraHeld {
     v4i b[NS][4];
@@ -284,7 +289,8 @@ __device__ __forceinline__ uint64_t lora_nan(int id, const v4f (&y)[NC]) {
 // zero, and V may lie beyond its first part's range, where the definition
 // gives an infinity or a number.  Called once behind the adapters' products of
 // a block (y, id, m, n0 as in lora_add); base(c) gives its scaled sums.  The
-// branch is not taken for finite operands.
+// branch is not taken for finite operands (2048 x 11008 x 4096, rank 32: 114
+// us, and 604 where X is NaN throughout and every result is formed twice).
 template <int IN, int NC, typename Base>
 __device__ __forceinline__ void lora_redo(const LoraArgs& L, int id, int m, int N, int n0,
                                           Base base, v4f (&y)[NC]) {

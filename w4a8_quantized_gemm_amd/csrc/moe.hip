@@ -8,8 +8,9 @@
 //     y    = (hq . W2[e]^T) sh sw2[e]
 //   Y[t] = sum_j weights[t][j] y(t, j)               (float32, j ascending)
 //
-// Every weight of a chosen expert is read once from HBM and nothing else is
-// of its size, so the weight stream bounds the layer.
+// The weights of the chosen experts are the bulk of the bytes, so their stream
+// bounds the layer.  A stream serves 16 rows of its expert, 32 or 64 where a
+// batch has that many per expert; an expert with more rows repeats it.
 #include "act_common.h"
 #include "launch.h"
 #include "mfma_common.h"
