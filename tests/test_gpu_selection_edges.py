@@ -245,3 +245,24 @@ def test_route_largest_batches(T, E, k):
             assert (part[1:] > part[:-1]).all() and (ids.view(-1)[part] == e).all()
     del x, r, ids, rows
     torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("dt", ["f16", "bf16"])
+@pytest.mark.parametrize("M,N,K,R", PATHS)
+def test_lora_rows_that_are_not_numbers(M, N, K, R, dt):
+    """Every third row holds a NaN: NaN throughout where it selects an
+    adapter, and the other rows keep their bits."""
+    say(f"lora NaN rows M={M} N={N} K={K} R={R} {dt}")
+    n = 3
+    p, rng, ad, X, A, B = bare(M, N, K, R, n, dt, M + R + 2)
+    X[:] = rng.integers(-8, 9, X.shape) / 8.0
+    A[:] = rng.integers(-8, 9, A.shape) / 64.0
+    B[:] = rng.integers(-8, 9, B.shape) / 64.0
+    good = adapters(p, X, A, B, ad, dt)
+    X[1::3, K // 2] = np.nan
+    got = adapters(p, X, A, B, ad, dt)
+    bad = np.zeros(M, bool)
+    bad[1::3] = True
+    assert np.isfinite(good).all()
+    assert np.isnan(got[bad & (ad >= 0)]).all()
+    np.testing.assert_array_equal(got[~bad], good[~bad])

@@ -314,7 +314,7 @@ __device__ __forceinline__ void mfma16_lora_epilogue(v4i (&acc)[MT / 16][4], uin
                 held, y[p]);
         }
 #pragma unroll
-        for (int p = 0; p < PB; ++p) nan |= lora_nan(id[p], y[p]);
+        for (int p = 0; p < PB; ++p) nan |= __ballot(lora_nan(id[p], y[p]));
 #pragma unroll
         for (int p = 0; p < PB; ++p)
 #pragma unroll
@@ -359,8 +359,7 @@ __device__ __forceinline__ void mfma16_lora_epilogue(v4i (&acc)[MT / 16][4], uin
                 y[cb][v] = (float)__builtin_bit_cast(
                     _Float16, (unsigned short)((v < 2 ? h.x : h.y) >> (16 * (v & 1))));
         }
-        if (lora_nan(id, y) == 0) continue;
-        lora_redo<LORA>(
+        const bool changed = lora_redo<LORA>(
             lora, id, m0 + row, N, n0,
             [&](int cb) {
                 const v4i sum = read_quad<0, MT / 16>(acc, rb, cb);
@@ -372,7 +371,7 @@ __device__ __forceinline__ void mfma16_lora_epilogue(v4i (&acc)[MT / 16][4], uin
                 return s;
             },
             y);
-        if (id < 0) continue;
+        if (!changed || id < 0) continue;
 #pragma unroll
         for (int cb = 0; cb < 4; ++cb) {
             unsigned short h[4];

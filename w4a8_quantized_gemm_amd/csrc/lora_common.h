@@ -274,14 +274,14 @@ __device__ __forceinline__ void lora_add_held(const LoraArgs& L, int id, int N, 
     }
 }
 
-// Lanes with a NaN among the results of a row that has an adapter.
+// Whether the results of a row that has an adapter hold a NaN (per lane).
 template <int NC>
-__device__ __forceinline__ uint64_t lora_nan(int id, const v4f (&y)[NC]) {
+__device__ __forceinline__ bool lora_nan(int id, const v4f (&y)[NC]) {
     bool nan = false;
 #pragma unroll
     for (int c = 0; c < NC; ++c)
         nan |= __builtin_isunordered(y[c][0], y[c][1]) || __builtin_isunordered(y[c][2], y[c][3]);
-    return __ballot(nan && id >= 0);
+    return nan && id >= 0;
 }
 
 // Results that came out as NaN are formed again, y = base + V . B in plain
@@ -289,19 +289,32 @@ __device__ __forceinline__ uint64_t lora_nan(int id, const v4f (&y)[NC]) {
 // zero, and V may lie beyond its first part's range, where the definition
 // gives an infinity or a number.  Called once behind the adapters' products of
 // a block (y, id, m, n0 as in lora_add); base(c) gives its scaled sums.  The
-// branch is not taken for finite operands (2048 x 11008 x 4096, rank 32: 114
-// us, and 604 where X is NaN throughout and every result is formed twice).
+// branch is not taken for finite operands, and rows whose V holds a NaN, whose
+// results are NaN, are left (2048 x 11008 x 4096, rank 32: 108 us, 203 where
+// every 16th row of X is NaN, 224 where all are; formed again, 400 and 604).
+// True where y may have changed, in any lane.
 template <int IN, int NC, typename Base>
-__device__ __forceinline__ void lora_redo(const LoraArgs& L, int id, int m, int N, int n0,
+__device__ __forceinline__ bool lora_redo(const LoraArgs& L, int id, int m, int N, int n0,
                                           Base base, v4f (&y)[NC]) {
-    if (__builtin_expect(lora_nan(id, y) == 0, 1)) return;
+    bool sound = lora_nan(id, y);
+    if (__builtin_expect(__ballot(sound) == 0, 1)) return false;
+    const float* v = L.V + (size_t)m * L.R;
+    if (sound)  // a row with a NaN in V has NaN results
+        for (int r = 0; r < L.R; r += 8) {
+            const v4f a = *reinterpret_cast<const v4f*>(v + r);
+            const v4f b = *reinterpret_cast<const v4f*>(v + r + 4);
+            sound = sound && !__builtin_isunordered(a[0], a[1]) &&
+                    !__builtin_isunordered(a[2], a[3]) && !__builtin_isunordered(b[0], b[1]) &&
+                    !__builtin_isunordered(b[2], b[3]);
+        }
+    if (__ballot(sound) == 0) return false;
     unsigned redo = 0;  // bit 4 c + q
 #pragma unroll
     for (int c = 0; c < NC; ++c) {
         const v4f s = base(c);
 #pragma unroll
         for (int q = 0; q < 4; ++q)
-            if (id >= 0 && y[c][q] != y[c][q]) {
+            if (sound && y[c][q] != y[c][q]) {
                 redo |= 1u << (4 * c + q);
                 y[c][q] = s[q];
             }
@@ -313,7 +326,6 @@ __device__ __forceinline__ void lora_redo(const LoraArgs& L, int id, int m, int 
         if ((redo >> k) & 1) {
             const size_t row = (size_t)id * N + n0 + 16 * (k >> 2) + 4 * G + (k & 3);
             const uint8_t* w = reinterpret_cast<const uint8_t*>(L.B) + row * L.R * 2;
-            const float* v = L.V + (size_t)m * L.R;
 #pragma clang loop unroll(disable)
             for (int r = 0; r < L.R; r += 8) {
                 const v4i b = load16(w + 2 * r);
@@ -332,6 +344,7 @@ __device__ __forceinline__ void lora_redo(const LoraArgs& L, int id, int m, int 
             for (int q = 0; q < 4; ++q)
                 if (k == 4 * c + q && ((redo >> k) & 1)) y[c][q] += sum;
     }
+    return true;
 }
 
 }  // namespace w4a8
