@@ -477,6 +477,93 @@ w4a8_status_t w4a8_gemm_lora(const void* X, int in_type, const uint8_t* wq,
                              int K, int group, void* workspace,
                              size_t workspace_bytes, hipStream_t stream);
 
+/*
+ * Between and around the projections of a layer: the norms, gate, residual
+ * sum and quantisation that lie between two of them (w4a8_norm_quant), and
+ * the gated feed-forward block (w4a8_ffn).  The conventions above hold;
+ * outputs and workspace overlap no other argument, except that Xout may be X.
+ */
+enum { W4A8_NORM_RMS = 0, W4A8_NORM_LAYER = 1 };
+enum {
+    W4A8_NORM_OUT_F32 = 0, /* = W4A8_IN_* */
+    W4A8_NORM_OUT_F16 = 1,
+    W4A8_NORM_OUT_BF16 = 2,
+    W4A8_NORM_OUT_INT8 = 3,
+    W4A8_NORM_OUT_E4M3 = 4
+};
+
+/*
+ * Residual sum and norms, with the rows that the next projection takes.  Per
+ * row m of K elements, every line one float32 operation per element, rounded
+ * by itself:
+ *   b  = Y[m];           b = norm(b; y_weight, y_bias)  if y_weight
+ *                        b = b gate[g]                  if gate
+ *   x' = x_scale X[m] + y_scale b;   Xout[m] = x' in x_type
+ *        (Y NULL: x' = x_scale X[m], and Xout is not used)
+ *   n  = x', or norm(x'; weight, bias) if weight
+ *   out[m] = n rounded once to a floating type, or
+ *     W4A8_NORM_OUT_INT8: sx[m] = max|n| / 127, out = the int8 codes of
+ *       w4a8_quant_act; W4A8_NORM_OUT_E4M3: sx[m] = max|n| / 448, out = the
+ *       codes of w4fp8_quant_act (each from the float32 n; sx = 1 where n is
+ *       zero throughout).
+ * norm(v; w, c), float32 but for the sums, which are float64:
+ *   W4A8_NORM_RMS:   r = float32(1 / sqrt(mean(v^2) + eps));  (v r) w + c
+ *   W4A8_NORM_LAYER: u = float32(mean(v)), d = v - u,
+ *                    r = float32(1 / sqrt(mean(d^2) + eps));  (d r) w + c
+ *   c = NULL adds nothing.  Weights and biases are float32 [K].
+ * The float64 sums make codes and scales the same on every path of the
+ * library: a function of the inputs alone.
+ *   X, Xout: [M][K] of x_type; Y: [M][K], gate: [gate_rows][K] of y_type
+ *     (W4A8_IN_*; not read with Y NULL).
+ *   g = gate_ids[m] with gate_ids (int32 [M]; a value outside [0, gate_rows)
+ *     selects no gate: that row's factor is 1), else m, or 0 if gate_rows is 1.
+ *   A row whose n is not finite throughout gets sx = NaN and codes 0: the
+ *     GEMMs return NaN for it, and no other row is affected.
+ * K % 16 == 0; eps > 0; eps, x_scale and y_scale finite (W4A8_ERR_UNSUPPORTED
+ * otherwise); gate_rows is 1 or M without gate_ids.  W4A8_ERR_NULL_PTR also for
+ * a bias without its weight, and for y_weight or gate without Y.  X, Y, gate, Xout, out 16-byte
+ * aligned, the others 4-byte.
+ */
+w4a8_status_t w4a8_norm_quant(const void* X, int x_type, const void* Y,
+                              int y_type, const float* y_weight,
+                              const float* y_bias, const void* gate,
+                              int gate_rows, const int32_t* gate_ids,
+                              float x_scale, float y_scale,
+                              const float* weight, const float* bias, int kind,
+                              float eps, void* Xout, void* out, int out_type,
+                              float* sx, int M, int K, hipStream_t stream);
+
+enum { W4A8_ACT_SILU = 0, W4A8_ACT_GELU = 1 };
+
+/*
+ * A gated feed-forward block:
+ *   g, u = ((exact int32 product of Xq[m] and W13) * sx[m]) * sw13 (float32)
+ *   h    = act(g) * u: W4A8_ACT_SILU  g / (1 + exp(-g)),
+ *                      W4A8_ACT_GELU  g / (1 + exp(-z)) with
+ *                      z = 2 sqrt(2 / pi) g (1 + 0.044715 g^2) (the tanh form)
+ *   hq, sh = INT8 of h per row as w4a8_quant_act
+ *   Y[m] = ((exact int32 product of hq and W2) * sh) * sw2, rounded once to
+ *          out_type (W4A8_IN_F16 or W4A8_IN_BF16)
+ * Xq int8 [M][H], sx float32 [M] from w4a8_norm_quant or w4a8_quant_act; wq13,
+ * s13, a13, sw13: w4a8_pack (LQQ) of W13 [2F][H], gate rows 0..F-1, up rows
+ * F..2F-1; wq2, s2, a2, sw2: of W2 [H][F]; one group size for both.  A row
+ * whose sx is not finite, or whose h overflows float32, gives NaN (other rows
+ * are unaffected).
+ * H % 128 = 0, F % 128 = 0, both <= W4A8_EXACT_MAX_K, 2 F H < 2^32, M H and
+ * M F < 2^31.  Xq, Y and the byte arrays 16-byte aligned, the others 4-byte.
+ * workspace: w4a8_ffn_workspace_size bytes, 16-byte aligned, contents ignored
+ * and undefined afterwards; calls that share one must be ordered on one
+ * stream.
+ */
+size_t w4a8_ffn_workspace_size(int M, int H, int F);
+w4a8_status_t w4a8_ffn(const int8_t* Xq, const float* sx, const uint8_t* wq13,
+                       const uint8_t* s13, const uint8_t* a13,
+                       const float* sw13, const uint8_t* wq2,
+                       const uint8_t* s2, const uint8_t* a2, const float* sw2,
+                       int act, void* Y, int out_type, int M, int H, int F,
+                       int group, void* workspace, size_t workspace_bytes,
+                       hipStream_t stream);
+
 /* Static English text for a status code (never NULL). */
 const char* w4a8_status_str(w4a8_status_t status);
 

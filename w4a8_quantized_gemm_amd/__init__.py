@@ -39,6 +39,9 @@ OUT_F16, OUT_I32 = 0, 1
 OUT_BF16, OUT_F32 = 0, 1
 IN_F32, IN_F16, IN_BF16 = 0, 1, 2
 ABL_LQQ, ABL_AFFINE16, ABL_LQQ_COARSE = 0, 1, 2
+NORM_RMS, NORM_LAYER = 0, 1
+NORM_OUT_F32, NORM_OUT_F16, NORM_OUT_BF16, NORM_OUT_INT8, NORM_OUT_E4M3 = range(5)
+ACT_SILU, ACT_GELU = 0, 1
 LAYOUT_VERSION = 1
 MAX_EXPERTS, MAX_TOPK, MOE_MAX_TOKENS, LORA_MAX_RANK = 512, 16, 256, 128
 EXACT_MAX_K = 131072
@@ -50,6 +53,7 @@ EXPORTS = ("w4a8_pack", "w4a8_quant_act", "w4fp8_quant_act",
            "w4fp8g_gemm", "w8a8_pack", "w8a8_gemm",
            "w4a8_route_workspace_size", "w4a8_route", "w4a8_moe_workspace_size", "w4a8_moe",
            "w4a8_gemm_lora_workspace_size", "w4a8_gemm_lora",
+           "w4a8_norm_quant", "w4a8_ffn_workspace_size", "w4a8_ffn",
            "w4a8_status_str", "w4a8_last_hip_error", "w4a8_layout_version")
 
 _P, _I, _Z = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t
@@ -81,6 +85,13 @@ lib.w4a8_gemm_lora_workspace_size.argtypes = [_I, _I, _I, _I]
 lib.w4a8_gemm_lora_workspace_size.restype = _Z
 lib.w4a8_gemm_lora.argtypes = [_P, _I, _P, _P, _P, _P, _P, _P, _P, _I, _I, _P, _P, _I, _I, _I,
                                _I, _P, _Z, _P]
+_F = ctypes.c_float
+lib.w4a8_norm_quant.argtypes = [_P, _I, _P, _I, _P, _P, _P, _I, _P, _F, _F, _P, _P, _I, _F, _P, _P,
+                                _I, _P, _I, _I, _P]
+lib.w4a8_ffn_workspace_size.argtypes = [_I, _I, _I]
+lib.w4a8_ffn_workspace_size.restype = _Z
+lib.w4a8_ffn.argtypes = [_P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _I, _P, _I, _I, _I, _I, _I, _P, _Z,
+                         _P]
 lib.w4a8_status_str.argtypes = [_I]
 lib.w4a8_status_str.restype = ctypes.c_char_p
 lib.w4a8_last_hip_error.restype = _I
@@ -88,7 +99,8 @@ lib.w4a8_layout_version.restype = _I
 for _n in ("w4a8_pack", "w4a8_quant_act", "w4fp8_quant_act", "w4a8_quant_act_ex",
            "w4fp8_quant_act_ex", "w4a8_gemm", "w4a8_gemm_noalloc", "w4a8_gemm_ablation", "w4a8_gemm_grouped",
            "w4fp8_gemm", "w4fp8g_pack", "w4fp8g_gemm", "w8a8_pack", "w8a8_gemm",
-           "w4a8_gemm_plan", "w4a8_route", "w4a8_moe", "w4a8_gemm_lora"):
+           "w4a8_gemm_plan", "w4a8_route", "w4a8_moe", "w4a8_gemm_lora", "w4a8_norm_quant",
+           "w4a8_ffn"):
     getattr(lib, _n).restype = _I
 
 assert lib.w4a8_layout_version() == LAYOUT_VERSION
@@ -679,4 +691,131 @@ def gemm_lora(X, packed, lora, adapter, out=None, workspace=None, stream=None):
                                   lora["scale"].data_ptr(), n, R, adapter.data_ptr(),
                                   out.data_ptr(), M, N, K, packed["group"], ws_ptr, ws_bytes,
                                   _raw_stream(dev.index)), "w4a8_gemm_lora")
+    return out
+
+
+# ---------------------------------------- between and around the projections ----
+#
+# Devices, streams and buffers as above.
+
+_NORM_OUT_DTYPE = {NORM_OUT_F32: torch.float32, NORM_OUT_F16: torch.float16,
+                   NORM_OUT_BF16: torch.bfloat16, NORM_OUT_INT8: torch.int8,
+                   NORM_OUT_E4M3: torch.uint8}
+
+
+def _opt(t, dtype, shape, device, name):
+    """Address of an optional tensor, checked."""
+    if t is None:
+        return None
+    _ready(t, dtype, shape, device, name)
+    return t.data_ptr()
+
+
+def norm_quant(x, weight=None, bias=None, y=None, y_weight=None, y_bias=None, gate=None,
+               gate_ids=None, x_scale: float = 1.0, y_scale: float = 1.0, eps: float = 1e-5,
+               kind: int = NORM_RMS, out_type: int = NORM_OUT_INT8, out=None, stream=None):
+    """w4a8_norm_quant: x' = x_scale x + y_scale (gate norm(y)), and the rows
+    of norm(x') that the next projection takes.
+
+    x: [M][K] residual stream, y: [M][K] the block's output (None: no block),
+    each float32, float16 or bfloat16.  weight / bias and y_weight / y_bias:
+    float32 [K] of the norm of x' and of y (weight None: no such norm), of the
+    same `kind`.  gate: [rows][K] in y's type; row m takes gate[gate_ids[m]]
+    (int32 [M]; outside [0, rows): no gate), without gate_ids its own row
+    (rows = M) or the only one.
+
+    Returns a dict with out ([M][K]: int8 or e4m3 bytes for the GEMMs, or a
+    floating type for moe and gemm_lora), sx (float32 [M] scales; None for
+    floating types) and x (the new residual stream in x's type; x itself
+    without y).  `out`: such a dict to write into; its x may be the input x."""
+    xt = _float_type(x, "x")
+    _on_gpu(x, "x")
+    M, K = x.shape
+    dev = x.device
+    _ready(x, x.dtype, (M, K), dev, "x")
+    dtype = _NORM_OUT_DTYPE.get(out_type)
+    if dtype is None:
+        raise ValueError(f"out_type must be one of the NORM_OUT_ constants, got {out_type}")
+    quantised = out_type >= NORM_OUT_INT8
+    yt = rows = 0
+    y_ptr = gate_ptr = ids_ptr = None
+    if y is not None:
+        yt = _float_type(y, "y")
+        _ready(y, y.dtype, (M, K), dev, "y")
+        y_ptr = y.data_ptr()
+        if gate is not None:
+            if not isinstance(gate, torch.Tensor) or gate.dim() != 2:
+                raise ValueError("gate must be a 2-D tensor [rows][K]")
+            rows = gate.shape[0]
+            if rows < 1 or (gate_ids is None and rows not in (1, M)):
+                raise ValueError(f"gate must have 1 or {M} rows, or gate_ids; got {rows}")
+            _ready(gate, y.dtype, (rows, K), dev, "gate")
+            gate_ptr = gate.data_ptr()
+            ids_ptr = _opt(gate_ids, torch.int32, (M,), dev, "gate_ids")
+        elif gate_ids is not None:
+            raise ValueError("gate_ids needs a gate")
+    elif y_weight is not None or gate is not None or gate_ids is not None:
+        raise ValueError("y_weight, gate and gate_ids need y")
+    if (bias is not None and weight is None) or (y_bias is not None and y_weight is None):
+        raise ValueError("a bias needs its weight")
+    with _context(dev, stream):
+        if out is None:
+            out = {"out": torch.empty((M, K), dtype=dtype, device=dev),
+                   "sx": torch.empty(M, dtype=torch.float32, device=dev) if quantised else None,
+                   "x": x if y is None else torch.empty((M, K), dtype=x.dtype, device=dev)}
+        else:
+            _ready(out["out"], dtype, (M, K), dev, "out['out']")
+            if quantised:
+                _ready(out["sx"], torch.float32, (M,), dev, "out['sx']")
+            if y is not None:
+                _ready(out["x"], x.dtype, (M, K), dev, "out['x']")
+        _check(lib.w4a8_norm_quant(
+            x.data_ptr(), xt, y_ptr, yt, _opt(y_weight, torch.float32, (K,), dev, "y_weight"),
+            _opt(y_bias, torch.float32, (K,), dev, "y_bias"), gate_ptr, rows, ids_ptr, x_scale,
+            y_scale, _opt(weight, torch.float32, (K,), dev, "weight"),
+            _opt(bias, torch.float32, (K,), dev, "bias"), kind, eps,
+            None if y is None else out["x"].data_ptr(), out["out"].data_ptr(), out_type,
+            out["sx"].data_ptr() if quantised else None, M, K, _raw_stream(dev.index)),
+            "w4a8_norm_quant")
+    return out
+
+
+def ffn_workspace_size(M: int, H: int, F: int) -> int:
+    return int(lib.w4a8_ffn_workspace_size(M, H, F))
+
+
+def ffn(Xq, sx, w13, w2, act: int = ACT_SILU, dtype=torch.float16, out=None, workspace=None,
+        stream=None):
+    """w4a8_ffn: the gated feed-forward block act(X W13_gate) (X W13_up), per-row
+    INT8 of it, times W2.
+
+    Xq, sx: INT8 rows [M][H] and their scales from norm_quant or quant_act; w13
+    and w2 from pack on [2F][H] (gate rows, then up rows) and [H][F].  Returns Y
+    [M][H] in `dtype` (float16 or bfloat16), or writes into `out`."""
+    if not isinstance(Xq, torch.Tensor):
+        raise TypeError("Xq must be a torch.Tensor")
+    _on_gpu(Xq, "Xq")
+    M, H = Xq.shape
+    dev = Xq.device
+    F, g = w2["K"], w13["group"]
+    if w2["group"] != g:
+        raise ValueError("w13 and w2 must have the same group size")
+    if w13["N"] != 2 * F or w13["K"] != H or w2["N"] != H:
+        raise ValueError(f"w13 must be [2F][H] and w2 [H][F] with H = {H}; got "
+                         f"[{w13['N']}][{w13['K']}] and [{w2['N']}][{w2['K']}]")
+    _ready(Xq, torch.int8, (M, H), dev, "Xq")
+    _ready(sx, torch.float32, (M,), dev, "sx")
+    for p, name in ((w13, "w13"), (w2, "w2")):
+        _packed_ready(p, ("wq", "s_u8", "a_u8", "sw"), 1, dev, name)
+    with _context(dev, stream):
+        if out is None:
+            out = torch.empty((M, H), dtype=dtype, device=dev)
+        ot = _float_type(out, "out", _HALF_TYPES)
+        _ready(out, out.dtype, (M, H), dev, "out")
+        ws, ws_ptr, ws_bytes = _workspace(workspace, ffn_workspace_size, (M, H, F), dev)
+        _check(lib.w4a8_ffn(Xq.data_ptr(), sx.data_ptr(), w13["wq"].data_ptr(),
+                            w13["s_u8"].data_ptr(), w13["a_u8"].data_ptr(), w13["sw"].data_ptr(),
+                            w2["wq"].data_ptr(), w2["s_u8"].data_ptr(), w2["a_u8"].data_ptr(),
+                            w2["sw"].data_ptr(), act, out.data_ptr(), ot, M, H, F, g, ws_ptr,
+                            ws_bytes, _raw_stream(dev.index)), "w4a8_ffn")
     return out

@@ -3,6 +3,7 @@
 // largest value of a workgroup.
 #pragma once
 #include "device_common.h"
+#include "wave_common.h"
 
 namespace w4a8 {
 
@@ -15,6 +16,27 @@ __device__ __forceinline__ int quant_sym(float x, float s, float qmax) {
     float v = __builtin_rintf(__fdiv_rn(x, s));
     v = fminf(fmaxf(v, -qmax), qmax);
     return (int)v;
+}
+
+// Absolute maximum as the bits of a non-negative float: an integer maximum,
+// so a NaN (whose bits lie above infinity's) is not lost.
+__device__ __forceinline__ unsigned abs_bits(float v) {
+    return __builtin_bit_cast(unsigned, v) & 0x7FFFFFFFu;
+}
+__device__ __forceinline__ unsigned block_max_bits(unsigned m) {
+    __shared__ unsigned part[16];
+    m = wave_reduce(m, MaxU32{});
+    if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = m;
+    __syncthreads();
+    for (int w = 0; w < (int)(blockDim.x >> 6); ++w) m = MaxU32{}(m, part[w]);
+    __syncthreads();
+    return m;
+}
+// Scale of a row: max / qmax, 1 for an all-zero row, and NaN for a row with
+// an element that is not finite (all of the row's results are NaN then).
+__device__ __forceinline__ float row_scale_bits(unsigned m, float qmax = 127.0f) {
+    if (m >= 0x7F800000u) return __builtin_nanf("");
+    return scale_of(__builtin_bit_cast(float, m), qmax);
 }
 
 // Four quant_sym(v, s, 127) codes as the bytes of a dword, in fewer

@@ -5,6 +5,7 @@
 #include <stdint.h>
 
 #include <atomic>
+#include <cmath>
 #include <cstring>
 
 #include "launch.h"
@@ -157,6 +158,14 @@ bool valid_moe(int T, int E, int k, int H, int F) {
     return T >= 0 && T <= W4A8_MOE_MAX_TOKENS && E >= 1 && E <= W4A8_MAX_EXPERTS && k >= 1 &&
            k <= W4A8_MAX_TOPK && H > 0 && H % 128 == 0 && F > 0 && F % 128 == 0 &&
            exact_sum(H) && exact_sum(F) && 2LL * F * H < (1LL << 32);
+}
+
+// A gated feed-forward block: the limits of its two GEMMs, W13 [2F][H] and
+// W2 [H][F].
+bool valid_ffn(int M, int H, int F) {
+    return M >= 0 && H > 0 && H % 128 == 0 && F > 0 && F % 128 == 0 && exact_sum(H) &&
+           exact_sum(F) && 2LL * F * H < (1LL << 32) && (long long)M * H < (1LL << 31) &&
+           (long long)M * F < (1LL << 31);
 }
 
 bool valid_rank(int R) { return R >= 8 && R <= W4A8_LORA_MAX_RANK && R % 8 == 0; }
@@ -658,4 +667,137 @@ W4A8_EXPORT w4a8_status_t w4a8_gemm_lora(const void* X, int in_type, const uint8
     if (e != hipSuccess) return hip_status(e);
     return hip_status(w4a8::launch_lora_join(acc, lay.tiles ? lay.plan.splits : 1, sx, sw, in_type,
                                              lora, M, N, Y, stream));
+}
+
+W4A8_EXPORT w4a8_status_t w4a8_norm_quant(
+    const void* X, int x_type, const void* Y, int y_type, const float* y_weight,
+    const float* y_bias, const void* gate, int gate_rows, const int32_t* gate_ids, float x_scale,
+    float y_scale, const float* weight, const float* bias, int kind, float eps, void* Xout,
+    void* out, int out_type, float* sx, int M, int K, hipStream_t stream) {
+    if (!valid_in_type(x_type) || (Y && !valid_in_type(y_type)) ||
+        (kind != W4A8_NORM_RMS && kind != W4A8_NORM_LAYER) || out_type < W4A8_NORM_OUT_F32 ||
+        out_type > W4A8_NORM_OUT_E4M3)
+        return W4A8_ERR_UNSUPPORTED;
+    if (!(eps > 0.0f) || !std::isfinite(eps) || !std::isfinite(x_scale) || !std::isfinite(y_scale))
+        return W4A8_ERR_UNSUPPORTED;
+    if (M < 0 || K <= 0 || K % 16 != 0) return W4A8_ERR_SHAPE;
+    if (gate && (gate_rows < 1 || (!gate_ids && gate_rows != 1 && gate_rows != M)) && M > 0)
+        return W4A8_ERR_SHAPE;
+    if (M == 0) return W4A8_OK;  // nothing to read or write
+    const bool quantised = out_type >= W4A8_NORM_OUT_INT8;
+    if (!X || !out || (quantised && !sx) || (Y && !Xout)) return W4A8_ERR_NULL_PTR;
+    if (!Y && (y_weight || gate)) return W4A8_ERR_NULL_PTR;
+    if ((y_bias && !y_weight) || (bias && !weight) || (gate_ids && !gate)) return W4A8_ERR_NULL_PTR;
+    if (!aligned16(X) || !aligned16(out) || (Y && (!aligned16(Y) || !aligned16(Xout))) ||
+        !aligned16(gate))
+        return W4A8_ERR_ALIGNMENT;
+    if (!aligned4(y_weight) || !aligned4(y_bias) || !aligned4(gate_ids) || !aligned4(weight) ||
+        !aligned4(bias) || (quantised && !aligned4(sx)))
+        return W4A8_ERR_ALIGNMENT;
+    w4a8_status_t d = check_device();
+    if (d != W4A8_OK) return d;
+    w4a8::NormArgs a;
+    a.x = X;
+    a.y = Y;
+    a.y_weight = y_weight;
+    a.y_bias = y_bias;
+    a.gate = gate;
+    a.gate_ids = gate_ids;
+    a.weight = weight;
+    a.bias = bias;
+    a.xout = Xout;
+    a.out = out;
+    a.sx = sx;
+    a.gate_rows = gate_rows;
+    a.layer = kind == W4A8_NORM_LAYER;
+    a.out_type = out_type;
+    a.M = M;
+    a.K = K;
+    a.x_scale = x_scale;
+    a.y_scale = y_scale;
+    a.eps = eps;
+    return hip_status(w4a8::launch_norm_quant(a, x_type, y_type, stream));
+}
+
+namespace {
+
+// Workspace of the feed-forward block: the INT8 rows of h and their scales,
+// and the int32 sums of the gate and up products.
+struct FfnLayout {
+    size_t hq, sh, acc, down, bytes;
+    bool tiles, down_tiles;
+    w4a8::MfmaPlan plan{}, down_plan{};
+    FfnLayout(int M, int H, int F) {
+        size_t o = 0;
+        auto take = [&](size_t n) {
+            const size_t at = o;
+            o += (n + 255) & ~(size_t)255;
+            return at;
+        };
+        hq = take((size_t)M * F);
+        sh = take((size_t)M * sizeof(float));
+        tiles = use_mfma_tiles(M, 2 * F, H);
+        if (tiles) plan = w4a8::plan_w4a8_mfma(M, 2 * F, H);
+        down_tiles = use_mfma_tiles(M, H, F);
+        if (down_tiles) down_plan = w4a8::plan_w4a8_mfma(M, H, F, true);
+        acc = take((size_t)plan_parts() * M * 2 * F * sizeof(int));
+        down = take(down_plan.workspace);
+        bytes = o;
+    }
+    int plan_parts() const { return tiles ? plan.splits : 1; }
+};
+
+}  // namespace
+
+W4A8_EXPORT size_t w4a8_ffn_workspace_size(int M, int H, int F) {
+    if (!valid_ffn(M, H, F) || M == 0) return 0;
+    return FfnLayout(M, H, F).bytes;
+}
+
+W4A8_EXPORT w4a8_status_t w4a8_ffn(const int8_t* Xq, const float* sx, const uint8_t* wq13,
+                                   const uint8_t* s13, const uint8_t* a13, const float* sw13,
+                                   const uint8_t* wq2, const uint8_t* s2, const uint8_t* a2,
+                                   const float* sw2, int act, void* Y, int out_type, int M, int H,
+                                   int F, int group, void* workspace, size_t workspace_bytes,
+                                   hipStream_t stream) {
+    if ((out_type != W4A8_IN_F16 && out_type != W4A8_IN_BF16) ||
+        (act != W4A8_ACT_SILU && act != W4A8_ACT_GELU))
+        return W4A8_ERR_UNSUPPORTED;
+    if (!valid_ffn(M, H, F) || !valid_group(group)) return W4A8_ERR_SHAPE;
+    if (M == 0) return W4A8_OK;  // nothing to read or write
+    if (!Xq || !sx || !Y || !wq13 || !s13 || !a13 || !sw13 || !wq2 || !s2 || !a2 || !sw2)
+        return W4A8_ERR_NULL_PTR;
+    if (!aligned16(Xq) || !aligned16(Y) || !aligned16(wq13) || !aligned16(s13) ||
+        !aligned16(a13) || !aligned16(wq2) || !aligned16(s2) || !aligned16(a2))
+        return W4A8_ERR_ALIGNMENT;
+    if (!aligned4(sx) || !aligned4(sw13) || !aligned4(sw2)) return W4A8_ERR_ALIGNMENT;
+    const FfnLayout lay(M, H, F);
+    if (workspace_bytes < lay.bytes) return W4A8_ERR_WORKSPACE;
+    if (!workspace) return W4A8_ERR_NULL_PTR;
+    if (!aligned16(workspace)) return W4A8_ERR_ALIGNMENT;
+    w4a8_status_t d = check_device();
+    if (d != W4A8_OK) return d;
+    uint8_t* ws = reinterpret_cast<uint8_t*>(workspace);
+    int8_t* hq = reinterpret_cast<int8_t*>(ws + lay.hq);
+    float* sh = reinterpret_cast<float*>(ws + lay.sh);
+    int* acc = reinterpret_cast<int*>(ws + lay.acc);
+    hipError_t e;
+    if (lay.tiles && lay.plan.splits > 1)
+        e = w4a8::launch_w4a8_mfma16_partial(Xq, wq13, s13, a13, M, 2 * F, H, group, lay.plan, acc,
+                                             stream);
+    else if (lay.tiles)
+        e = w4a8::launch_w4a8_mfma(Xq, sx, wq13, s13, a13, sw13, acc, W4A8_OUT_I32, M, 2 * F, H,
+                                   group, lay.plan, nullptr, stream);
+    else
+        e = w4a8::launch_w4a8_stream(Xq, sx, wq13, s13, a13, sw13, acc, W4A8_OUT_I32, M, 2 * F, H,
+                                     group, choose_stream(M, 2 * F, H, 0, true), stream);
+    if (e != hipSuccess) return hip_status(e);
+    e = w4a8::launch_ffn_join(acc, lay.plan_parts(), sx, sw13, M, F, act, hq, sh, stream);
+    if (e != hipSuccess) return hip_status(e);
+    const int out = out_type == W4A8_IN_BF16 ? 2 : 0;
+    if (lay.down_tiles)
+        return hip_status(w4a8::launch_w4a8_mfma(hq, sh, wq2, s2, a2, sw2, Y, out, M, H, F, group,
+                                                 lay.down_plan, ws + lay.down, stream));
+    return hip_status(w4a8::launch_w4a8_stream(hq, sh, wq2, s2, a2, sw2, Y, out, M, H, F, group,
+                                               choose_stream(M, H, F, 0, true), stream));
 }

@@ -141,4 +141,14 @@ __device__ __forceinline__ unsigned short f32_to_bf16_bits(float v) {
     return (unsigned short)(u >> 16);
 }
 
+// float -> 16-bit output of a W4A8 GEMM: OUT 0 = fp16, 2 = bfloat16.
+template <int OUT>
+__device__ __forceinline__ unsigned short f32_to_out16_bits(float v) {
+    if constexpr (OUT == 2) {
+        asm("" : "+v"(v));
+        return f32_to_bf16_bits(v);
+    }
+    return f32_to_f16_bits(v);
+}
+
 }  // namespace w4a8

@@ -491,7 +491,7 @@ __global__ __launch_bounds__(256, 1) void w4a8_mfma_kernel(
     // (fp16) or 16-byte (int32) piece, rows padded by 16 bytes; each row is
     // then written as whole 16-byte pieces (final output, or this split's
     // int32 partial).
-    constexpr bool SCALED = (OUT == 0) && !PARTIAL;
+    constexpr bool SCALED = (OUT != 1) && !PARTIAL;
     if (SCALED) sxs[tid % MT] = (m0 + tid % MT < row_hi) ? sx[m0 + tid % MT] : 0.0f;
     float swv[2][4][4];
 #pragma unroll
@@ -522,7 +522,7 @@ __global__ __launch_bounds__(256, 1) void w4a8_mfma_kernel(
                     unsigned short hv[4];
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
-                        hv[e] = f32_to_f16_bits(((float)acc[rb][cb][4 * i + e] * sm) *
+                        hv[e] = f32_to_out16_bits<OUT>(((float)acc[rb][cb][4 * i + e] * sm) *
                                                 swv[cb][i][e]);
                     uint2 pk;
                     pk.x = hv[0] | ((unsigned)hv[1] << 16);
@@ -578,7 +578,7 @@ __global__ __launch_bounds__(256) void splitk_reduce_kernel(
         const float sm = sx[m];
         unsigned short hv[4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) hv[j] = f32_to_f16_bits(((float)acc[j] * sm) * sw[n + j]);
+        for (int j = 0; j < 4; ++j) hv[j] = f32_to_out16_bits<OUT>(((float)acc[j] * sm) * sw[n + j]);
         uint2 pk;
         pk.x = hv[0] | ((unsigned)hv[1] << 16);
         pk.y = hv[2] | ((unsigned)hv[3] << 16);
@@ -606,6 +606,7 @@ hipError_t launch_splitk_reduce(const int* part, int splits, int M, int N, const
                                 const float* sw, void* Y, int out_type, hipStream_t st) {
     if (M == 0) return hipSuccess;
     if (out_type == 1) return splitk_reduce_run<1>(part, splits, M, N, sx, sw, Y, st);
+    if (out_type == 2) return splitk_reduce_run<2>(part, splits, M, N, sx, sw, Y, st);
     return splitk_reduce_run<0>(part, splits, M, N, sx, sw, Y, st);
 }
 
@@ -726,6 +727,7 @@ static hipError_t run_mfma(const int8_t* X, const float* sx, const uint8_t* wq,
             else launch_tile<256, 0, false, DEC>(X, sx, wq, s_u8, a_u8, sw, Y, part, M, N, K, group, 1, st);
         } else {
             if (out_type == 1) launch_tile<128, 1, false, DEC>(X, sx, wq, s_u8, a_u8, sw, Y, part, M, N, K, group, 1, st);
+            else if (out_type == 2 && std::is_same_v<DEC, DecLQQ>) launch_tile<128, 2, false>(X, sx, wq, s_u8, a_u8, sw, Y, part, M, N, K, group, 1, st);
             else launch_tile<128, 0, false, DEC>(X, sx, wq, s_u8, a_u8, sw, Y, part, M, N, K, group, 1, st);
         }
         return hipGetLastError();

@@ -638,7 +638,7 @@ __device__ __forceinline__ void mfma16_body(
                                        reinterpret_cast<unsigned short*>(Y), m0, n0, row_hi, N);
         return;
     }
-    constexpr bool SCALED = (OUT == 0) && !PARTIAL;
+    constexpr bool SCALED = (OUT != 1) && !PARTIAL;
     if (SCALED) sxs[tid % MT] = (m0 + tid % MT < row_hi) ? sx[m0 + tid % MT] : 0.0f;
     float swv[4][4];
 #pragma unroll
@@ -701,7 +701,7 @@ __device__ __forceinline__ void mfma16_body(
                         unsigned short h[4];
 #pragma unroll
                         for (int v = 0; v < 4; ++v)
-                            h[v] = f32_to_f16_bits(((float)a[v] * sm) * swv[cb][v]);
+                            h[v] = f32_to_out16_bits<OUT>(((float)a[v] * sm) * swv[cb][v]);
                         uint2 pk;
                         pk.x = h[0] | ((unsigned)h[1] << 16);
                         pk.y = h[2] | ((unsigned)h[3] << 16);
@@ -787,6 +787,9 @@ static hipError_t run_mfma16(const int8_t* X, const float* sx, const uint8_t* wq
             if (out_type == 1)
                 launch_tile16<128, 1, false, W8, 2>(X, sx, wq, s_u8, a_u8, sw, Y, part, M, N, K,
                                                     group, 1, st, nullptr, 1, 0);
+            else if (!W8 && out_type == 2)
+                launch_tile16<128, 2, false, false, 2>(X, sx, wq, s_u8, a_u8, sw, Y, part, M, N, K,
+                                                       group, 1, st, nullptr, 1, 0);
             else
                 launch_tile16<128, 0, false, W8, 2>(X, sx, wq, s_u8, a_u8, sw, Y, part, M, N, K,
                                                     group, 1, st, nullptr, 1, 0);
@@ -797,15 +800,17 @@ static hipError_t run_mfma16(const int8_t* X, const float* sx, const uint8_t* wq
         return launch_splitk_reduce(part, plan.splits, M, N, sx, sw, Y, out_type, st);
     }
     if (plan.splits == 1) {
-#define T16(MT_, O_) \
-    launch_tile16<MT_, O_, false, W8>(X, sx, wq, s_u8, a_u8, sw, Y, part, M, N, K, group, 1, st, \
+#define T16(MT_, O_, W_) \
+    launch_tile16<MT_, O_, false, W_>(X, sx, wq, s_u8, a_u8, sw, Y, part, M, N, K, group, 1, st, \
                                       offsets, E, max_rows)
         if (plan.mt == 256) {
-            if (out_type == 1) T16(256, 1);
-            else T16(256, 0);
+            if (out_type == 1) T16(256, 1, W8);
+            else if (!W8 && out_type == 2) T16(256, 2, false);
+            else T16(256, 0, W8);
         } else {
-            if (out_type == 1) T16(128, 1);
-            else T16(128, 0);
+            if (out_type == 1) T16(128, 1, W8);
+            else if (!W8 && out_type == 2) T16(128, 2, false);
+            else T16(128, 0, W8);
         }
 #undef T16
         return hipGetLastError();

@@ -54,12 +54,16 @@ static hipError_t w4a8_stream_ntw(const int8_t* X, const float* sx, const uint8_
     if (ldsp) {
         if (out_type == 1) {
             if (group == 64) W4A8_LS(1, 64, true); else W4A8_LS(1, 128, true);
+        } else if (out_type == 2) {
+            if (group == 64) W4A8_LS(2, 64, true); else W4A8_LS(2, 128, true);
         } else {
             if (group == 64) W4A8_LS(0, 64, true); else W4A8_LS(0, 128, true);
         }
     } else {
         if (out_type == 1) {
             if (group == 64) W4A8_LS(1, 64, false); else W4A8_LS(1, 128, false);
+        } else if (out_type == 2) {
+            if (group == 64) W4A8_LS(2, 64, false); else W4A8_LS(2, 128, false);
         } else {
             if (group == 64) W4A8_LS(0, 64, false); else W4A8_LS(0, 128, false);
         }

@@ -19,6 +19,9 @@ hipError_t launch_act_int8(const void* X, int in_type, int M, int K, int8_t* Xq,
 hipError_t launch_act_e4m3(const void* X, int in_type, int M, int K, uint8_t* Xq, float* sx,
                            hipStream_t st);
 
+// out_type of the W4A8 launchers: 0 = fp16, 1 = int32 (W4A8_OUT_*), 2 = bfloat16
+// (not for grouped problems, W8A8 or the ablations; FP8 kinds have their own).
+
 // Streamed-tile GEMMs: one workgroup per (16*nt_per_wave rows of N, 16 rows
 // of M); `ks` waves split K and reduce in LDS.
 struct StreamCfg {
@@ -152,6 +155,30 @@ size_t moe_workspace(int T, int k, int H, int F);
 hipError_t launch_moe(const void* X, int in_type, const int* ids, const float* weights, int T,
                       int E, int k, const MoeWeights& w13, const MoeWeights& w2, void* Y,
                       int out_type, int H, int F, int group, void* workspace, hipStream_t st);
+
+// The norms, gate and residual sum between two projections, and the quantised
+// rows of the next one (include/w4a8.h).  y_weight / weight NULL: no norm.
+struct NormArgs {
+    const void* x;        // [M][K] residual stream
+    const void* y;        // [M][K] block output, or NULL
+    const float* y_weight;
+    const float* y_bias;
+    const void* gate;     // [gate_rows][K] of y's type, or NULL
+    const int* gate_ids;  // [M], or NULL
+    const float* weight;
+    const float* bias;
+    void* xout;
+    void* out;
+    float* sx;
+    int gate_rows, layer, out_type, M, K;  // out_type: W4A8_IN_*, 3 INT8, 4 e4m3
+    float x_scale, y_scale, eps;
+};
+hipError_t launch_norm_quant(const NormArgs& a, int x_type, int y_type, hipStream_t st);
+
+// Gated feed-forward block: h = act(gate) up of int32 sums [splits][M][2F]
+// (gate rows first), and its per-row INT8.
+hipError_t launch_ffn_join(const int* acc, int splits, const float* sx, const float* sw13, int M,
+                           int F, int act, int8_t* hq, float* sh, hipStream_t st);
 
 // Low-rank adapters: V [M][R] float32 = scale (X . A^T) of the rows that
 // select one, B [n_adapters][N][R] of in_type.

@@ -58,27 +58,6 @@ struct MoeLayout {
 
 }  // namespace
 
-// Absolute maximum as the bits of a non-negative float: an integer maximum,
-// so a NaN (whose bits lie above infinity's) is not lost.
-__device__ __forceinline__ unsigned abs_bits(float v) {
-    return __builtin_bit_cast(unsigned, v) & 0x7FFFFFFFu;
-}
-__device__ __forceinline__ unsigned block_max_bits(unsigned m) {
-    __shared__ unsigned part[16];
-    m = wave_reduce(m, MaxU32{});
-    if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = m;
-    __syncthreads();
-    for (int w = 0; w < (int)(blockDim.x >> 6); ++w) m = MaxU32{}(m, part[w]);
-    __syncthreads();
-    return m;
-}
-// Scale of a row: max / 127, 1 for an all-zero row, and NaN for a row with
-// an element that is not finite (all of the row's results are NaN then).
-__device__ __forceinline__ float row_scale_bits(unsigned m) {
-    if (m >= 0x7F800000u) return __builtin_nanf("");
-    return scale_of(__builtin_bit_cast(float, m), 127.0f);
-}
-
 template <int IN>
 __device__ __forceinline__ void quant_row(const void* row, int K, int8_t* out, float* scale) {
     unsigned m = 0;

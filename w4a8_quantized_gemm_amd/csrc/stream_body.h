@@ -49,7 +49,8 @@ __device__ __forceinline__ int xpiece(int R, int c) {
 //           group (fsc group-major [K/GROUP][N]; with 64-wide groups lane
 //           quarter G lies in group 2 kt + G/2), loaded with the weights,
 //           and the epilogue scales by tsc[0].
-// OUT: 0 = fp16 (INT8 kinds) or bf16 (FP8 kinds), 1 = int32 or float32.
+// OUT: 0 = fp16 (INT8 kinds) or bf16 (FP8 kinds), 1 = int32 or float32, 2 = bf16
+// (W4A8).
 constexpr int kWkLQQ = 0, kWkW8 = 1, kWkF8 = 2, kWkF8G = 3;
 
 // LORA (1: fp16, 2: bfloat16 adapters; W4A8 to fp16 only): the epilogue adds
@@ -385,7 +386,7 @@ __device__ __forceinline__ void stream_body(
                 reinterpret_cast<int*>(Y)[(size_t)m * N + n] = sum;
             } else {
                 const float y = ((float)sum * sx[m]) * sw[n];
-                reinterpret_cast<unsigned short*>(Y)[(size_t)m * N + n] = f32_to_f16_bits(y);
+                reinterpret_cast<unsigned short*>(Y)[(size_t)m * N + n] = f32_to_out16_bits<OUT>(y);
             }
         }
     }
