@@ -721,10 +721,11 @@ W4A8_EXPORT w4a8_status_t w4a8_norm_quant(
 
 namespace {
 
-// Workspace of the feed-forward block: the INT8 rows of h and their scales,
-// and the int32 sums of the gate and up products.
+// Workspace of the feed-forward block: the INT8 rows of h and their scales;
+// h itself and its partial maxima, or, where the gate and up products are
+// split over K or streamed, their int32 sums; the down product's own.
 struct FfnLayout {
-    size_t hq, sh, acc, down, bytes;
+    size_t hq, sh, h, tops, acc, down, bytes;
     bool tiles, down_tiles;
     w4a8::MfmaPlan plan{}, down_plan{};
     FfnLayout(int M, int H, int F) {
@@ -740,11 +741,13 @@ struct FfnLayout {
         if (tiles) plan = w4a8::plan_w4a8_mfma(M, 2 * F, H);
         down_tiles = use_mfma_tiles(M, H, F);
         if (down_tiles) down_plan = w4a8::plan_w4a8_mfma(M, H, F, true);
-        acc = take((size_t)plan_parts() * M * 2 * F * sizeof(int));
+        h = take(fused() ? (size_t)M * F * sizeof(float) : 0);
+        tops = take(fused() ? (size_t)M * (F / 32) * sizeof(unsigned) : 0);
+        acc = take(fused() ? 0 : (size_t)(tiles ? plan.splits : 1) * M * 2 * F * sizeof(int));
         down = take(down_plan.workspace);
         bytes = o;
     }
-    int plan_parts() const { return tiles ? plan.splits : 1; }
+    bool fused() const { return tiles && plan.splits == 1; }
 };
 
 }  // namespace
@@ -782,17 +785,24 @@ W4A8_EXPORT w4a8_status_t w4a8_ffn(const int8_t* Xq, const float* sx, const uint
     float* sh = reinterpret_cast<float*>(ws + lay.sh);
     int* acc = reinterpret_cast<int*>(ws + lay.acc);
     hipError_t e;
-    if (lay.tiles && lay.plan.splits > 1)
-        e = w4a8::launch_w4a8_mfma16_partial(Xq, wq13, s13, a13, M, 2 * F, H, group, lay.plan, acc,
-                                             stream);
-    else if (lay.tiles)
-        e = w4a8::launch_w4a8_mfma(Xq, sx, wq13, s13, a13, sw13, acc, W4A8_OUT_I32, M, 2 * F, H,
-                                   group, lay.plan, nullptr, stream);
-    else
-        e = w4a8::launch_w4a8_stream(Xq, sx, wq13, s13, a13, sw13, acc, W4A8_OUT_I32, M, 2 * F, H,
-                                     group, choose_stream(M, 2 * F, H, 0, true), stream);
-    if (e != hipSuccess) return hip_status(e);
-    e = w4a8::launch_ffn_join(acc, lay.plan_parts(), sx, sw13, M, F, act, hq, sh, stream);
+    if (lay.fused()) {
+        float* h = reinterpret_cast<float*>(ws + lay.h);
+        unsigned* tops = reinterpret_cast<unsigned*>(ws + lay.tops);
+        e = w4a8::launch_w4a8_mfma16_glu(Xq, sx, wq13, s13, a13, sw13, act, h, tops, M, F, H, group,
+                                         lay.plan.mt16 ? lay.plan.mt16 : lay.plan.mt, stream);
+        if (e != hipSuccess) return hip_status(e);
+        e = w4a8::launch_ffn_quant(h, tops, F / 32, M, F, hq, sh, stream);
+    } else {
+        if (lay.tiles)
+            e = w4a8::launch_w4a8_mfma16_partial(Xq, wq13, s13, a13, M, 2 * F, H, group, lay.plan,
+                                                 acc, stream);
+        else
+            e = w4a8::launch_w4a8_stream(Xq, sx, wq13, s13, a13, sw13, acc, W4A8_OUT_I32, M, 2 * F,
+                                         H, group, choose_stream(M, 2 * F, H, 0, true), stream);
+        if (e != hipSuccess) return hip_status(e);
+        e = w4a8::launch_ffn_join(acc, lay.tiles ? lay.plan.splits : 1, sx, sw13, M, F, act, hq, sh,
+                                  stream);
+    }
     if (e != hipSuccess) return hip_status(e);
     const int out = out_type == W4A8_IN_BF16 ? 2 : 0;
     if (lay.down_tiles)

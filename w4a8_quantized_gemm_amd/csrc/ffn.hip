@@ -46,6 +46,36 @@ __global__ __launch_bounds__(1024) void ffn_join_kernel(const int* __restrict__ 
     }
 }
 
+// INT8 of h.  A row's maximum is that of its `ntops` parts; blockIdx.y: part of
+// the row (few rows: more workgroups than rows).
+__global__ __launch_bounds__(256) void ffn_quant_kernel(const float* __restrict__ h,
+                                                        const unsigned* __restrict__ tops,
+                                                        int ntops, int F, int8_t* __restrict__ hq,
+                                                        float* __restrict__ sh) {
+    const size_t m = blockIdx.x;
+    unsigned top = 0;
+    for (int i = threadIdx.x; i < ntops; i += 256) top = MaxU32{}(top, tops[m * ntops + i]);
+    const float s = row_scale_bits(block_max_bits(top)), inv = __fdiv_rn(1.0f, s);
+    if (threadIdx.x == 0 && blockIdx.y == 0) sh[m] = s;
+    const v4f* row = reinterpret_cast<const v4f*>(h + m * F);
+    unsigned* out = reinterpret_cast<unsigned*>(hq + m * F);
+    for (int i = blockIdx.y * 256 + threadIdx.x; i < F / 4; i += 256 * gridDim.y) {
+        const v4f v = row[i];
+        out[i] = quant4_fast(v[0], v[1], v[2], v[3], s, inv);
+    }
+}
+
+hipError_t launch_ffn_quant(const float* h, const unsigned* tops, int ntops, int M, int F,
+                            int8_t* hq, float* sh, hipStream_t st) {
+    // about four workgroups per CU, each with four elements a thread at least
+    const int most = (F / 4 + 255) / 256;
+    int parts = (1024 + M - 1) / M;
+    if (parts > most) parts = most;
+    hipLaunchKernelGGL(ffn_quant_kernel, dim3(M, parts), dim3(256), 0, st, h, tops, ntops, F, hq,
+                       sh);
+    return hipGetLastError();
+}
+
 hipError_t launch_ffn_join(const int* acc, int splits, const float* sx, const float* sw13, int M,
                            int F, int act, int8_t* hq, float* sh, hipStream_t st) {
     const dim3 block(F / 4 < 1024 ? (F / 4 + 63) / 64 * 64 : 1024);

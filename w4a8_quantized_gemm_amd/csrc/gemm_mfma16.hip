@@ -38,6 +38,7 @@
 // (128 x 28672 x 8192: 48.0 -> 42.6 us).
 #include <type_traits>
 
+#include "ffn_common.h"
 #include "launch.h"
 #include "lora_common.h"
 #include "mfma_common.h"
@@ -84,6 +85,18 @@ __device__ __forceinline__ void mov16_step(const WRaw8x16& w, v4i (&B)[4][2]) {
     B[cb][U][d] = x;
 }
 
+// Gated feed-forward block: w[0..1] two tiles of the gate half, w[2..3] the
+// same two of the up half; sdw / adw[half] = their two parameter bytes.
+struct WRawGlu16 {
+    v4i w[4];
+    unsigned sdw[2], adw[2];
+};
+
+__device__ __forceinline__ void touch_raw16(const WRawGlu16& w) {
+    asm volatile("" ::"v"(w.w[0]), "v"(w.w[1]), "v"(w.w[2]), "v"(w.w[3]), "v"(w.sdw[0]),
+                 "v"(w.adw[0]), "v"(w.sdw[1]), "v"(w.adw[1]));
+}
+
 struct Par16 {
     unsigned s2[4], a4[4];  // per channel block: scale pair, offset quad
 };
@@ -107,6 +120,20 @@ __device__ __forceinline__ void par16_step(const WRaw16& w, Par16& p) {
     }
 }
 
+template <int K_>
+__device__ __forceinline__ void par16_step(const WRawGlu16& w, Par16& p) {
+    constexpr int cb = K_ / 2;
+    constexpr unsigned b = (unsigned)cb & 1;
+    if constexpr (K_ % 2 == 0) {
+        constexpr unsigned sel = b | 0x0C00u | (b << 16) | 0x0C000000u;
+        asm volatile("v_perm_b32 %0, 0, %1, %2" : "=v"(p.s2[cb]) : "v"(w.sdw[cb / 2]), "v"(sel));
+    } else {
+        asm volatile("v_perm_b32 %0, 0, %1, %2"
+                     : "=v"(p.a4[cb])
+                     : "v"(w.adw[cb / 2]), "v"(b * 0x01010101u));
+    }
+}
+
 // Decode step OP (0..55) producing B[*][U]: channel block cb = OP / 14,
 // packed dword d = 2U + dd with dd = (OP % 14) % 2, instruction
 // st = (OP % 14) / 2:
@@ -116,8 +143,8 @@ __device__ __forceinline__ void par16_step(const WRaw16& w, Par16& p) {
 // The two dwords' steps alternate, so no step reads the result of the one
 // just before it (the compiler puts a wait state between two dependent
 // assembly statements, not knowing what they are).
-template <int U, int OP>
-__device__ __forceinline__ void dec16_step(Tmp16& t, const WRaw16& w, const Par16& p,
+template <int U, int OP, class Raw>
+__device__ __forceinline__ void dec16_step(Tmp16& t, const Raw& w, const Par16& p,
                                            v4i (&B)[4][2]) {
     constexpr int cb = OP / 14, q = OP % 14, dd = q % 2, st = q / 2;
     constexpr int d = 2 * U + dd;
@@ -383,19 +410,70 @@ __device__ __forceinline__ void mfma16_lora_epilogue(v4i (&acc)[MT / 16][4], uin
     }
 }
 
+// Epilogue of a gated feed-forward block's first product: the wave's gate sums
+// lie in channel blocks 0 and 1, the up sums of the same 32 channels in 2 and
+// 3, so a lane forms act(gate) up of eight of its row's channels by itself.
+// Row blocks in a loop, as with adapters.
+template <int MT, int GLU>
+__device__ __forceinline__ void mfma16_glu_epilogue(v4i (&acc)[MT / 16][4], const float* sxs,
+                                                    const float* sw, const FfnOut& out, int m0,
+                                                    int c0, int row_hi, int F) {
+    constexpr int PB = 2;
+    const int lane = threadIdx.x & 63;
+    const int r = lane & 15, G = lane >> 4;
+    float w[4][4];
+#pragma unroll
+    for (int cb = 0; cb < 4; ++cb)
+#pragma unroll
+        for (int v = 0; v < 4; ++v)
+            w[cb][v] = sw[(cb < 2 ? 0 : F) + c0 + 16 * (cb & 1) + 4 * G + v];
+#pragma clang loop unroll(disable)
+    for (int rb = 0; rb < MT / 16; rb += PB) {
+        v4i cur[PB][4];
+        read_blocks<0, MT / 16, PB>(acc, rb, cur);
+#pragma unroll
+        for (int p = 0; p < PB; ++p) {
+            const int row = 16 * (rb + p) + r;
+            const size_t m = m0 + row;
+            const float sm = sxs[row];
+            v4f h[2];
+            unsigned top = 0;
+#pragma unroll
+            for (int c = 0; c < 2; ++c)
+#pragma unroll
+                for (int v = 0; v < 4; ++v) {
+                    const float x = gated<GLU - 1>(((float)cur[p][c][v] * sm) * w[c][v],
+                                                   ((float)cur[p][2 + c][v] * sm) * w[2 + c][v]);
+                    h[c][v] = x;
+                    top = MaxU32{}(top, abs_bits(x));
+                }
+            top = MaxU32{}(top, (unsigned)__shfl_xor((int)top, 16, 64));
+            top = MaxU32{}(top, (unsigned)__shfl_xor((int)top, 32, 64));
+            if ((int)m >= row_hi) continue;
+#pragma unroll
+            for (int c = 0; c < 2; ++c)
+                *reinterpret_cast<v4f*>(out.h + m * F + c0 + 16 * c + 4 * G) = h[c];
+            if (G == 0) out.tops[m * (F / 32) + c0 / 32] = top;
+        }
+    }
+}
+
 // W8: the W8A8 comparison on this skeleton (no decode, no parameters).
 // 128-row tiles fit two workgroups per CU (128 accumulator registers per
 // lane, at most 128 others), 256-row tiles one; with K parts (KIN = 2) the
 // X tiles take 96 KiB of LDS, one workgroup per CU.
 // LORA (1: fp16, 2: bfloat16 adapters): the epilogue adds each row's low-rank
 // adapter to its scaled sums before the one rounding.
-template <int MT, int OUT, int GROUP, bool PARTIAL, bool W8, int KIN, int LORA>
+// GLU (1: SiLU, 2: GELU): a workgroup takes 128 channels of the gate half and
+// the same of the up half of N = 2F, a wave 32 of each, and writes act(gate) up.
+template <int MT, int OUT, int GROUP, bool PARTIAL, bool W8, int KIN, int LORA, int GLU = 0>
 __device__ __forceinline__ void mfma16_body(
     const int8_t* __restrict__ X, const float* __restrict__ sx, const uint8_t* __restrict__ wq,
     const uint8_t* __restrict__ s_u8, const uint8_t* __restrict__ a_u8,
     const float* __restrict__ sw, void* __restrict__ Y, int* __restrict__ part, int M, int N,
     int K, int tiles_n, int tiles_m, int splits, const int* __restrict__ offsets,
-    const LoraArgs& lora) {
+    const LoraArgs& lora, const FfnOut& ffn = {}) {
+    static_assert(GLU == 0 || (!PARTIAL && !W8 && KIN == 1 && LORA == 0), "plain tiles");
     static_assert(LORA == 0 || (OUT == 0 && !PARTIAL && !W8 && KIN == 1), "one rounding to fp16");
     static_assert(KIN == 1 || (KIN == 2 && MT == 128), "K parts: 128-row tiles only");
     constexpr int RB = MT / 16;        // 16-row blocks per wave
@@ -403,12 +481,13 @@ __device__ __forceinline__ void mfma16_body(
     constexpr int CPT = MT / (8 * NWX);  // X loads (1 KiB per wave) per K-step
     constexpr int SLOTS = 8 * RB;      // matrix-core instructions per wave per K-step
     constexpr int GS = SLOTS / 2;      // slots per group u
-    constexpr int kLoads = W8 ? 8 : 6;  // raw loads per K-step: 4 tiles, s, a (W8: 8 halves)
+    // raw loads per K-step: 4 tiles, s, a (W8: 8 halves; GLU: s, a of both halves)
+    constexpr int kLoads = W8 || GLU ? 8 : 6;
     constexpr int NOPS = W8 ? 16 : 56;  // decode steps per group
     constexpr int NPAR = W8 ? 0 : 8;    // parameter steps
     constexpr int DQ0 = (NOPS + GS - 1) / GS;         // group-0 decode steps per slot
     constexpr int DQ1 = (NPAR + NOPS + GS - 1) / GS;  // group-1 parameter + decode steps per slot
-    using Raw = std::conditional_t<W8, WRaw8x16, WRaw16>;
+    using Raw = std::conditional_t<W8, WRaw8x16, std::conditional_t<GLU != 0, WRawGlu16, WRaw16>>;
     constexpr unsigned XB = MT * 128;     // bytes of one X tile
     constexpr unsigned XSTEP = KIN * XB;  // one K-step's X tiles, one per K part
     __shared__ __attribute__((aligned(1024))) uint8_t xs[3 * XSTEP];
@@ -438,7 +517,8 @@ __device__ __forceinline__ void mfma16_body(
     }
     const int m0 = row_lo + tc.tm * MT;
     if (m0 >= row_hi) return;  // whole workgroup: no rows of this expert here
-    const int n0 = tc.tn * (kNT / KIN) + wc * kColsPerWave;
+    const int n0 = GLU ? tc.tn * (kNT / 2) + wc * (kColsPerWave / 2)
+                       : tc.tn * (kNT / KIN) + wc * kColsPerWave;
     const int KTall = K / kTileK;
     // K is cut into splits * KIN parts; this wave takes part ks * KIN + kp
     const int parts = splits * KIN;
@@ -493,6 +573,11 @@ __device__ __forceinline__ void mfma16_body(
     // the lane's 32 K columns lie in the K-step's group G / 2 when GROUP = 64
     const unsigned pvoff = 4u * (unsigned)r + (GROUP == 64 ? 64u * (unsigned)(G >> 1) : 0u);
     const unsigned ppanel = 64u * (unsigned)(n0 >> 6) * (unsigned)groups;
+    // GLU: the up half's tiles and panels lie F = N / 2 channels on (whole
+    // panels), and a wave's two tiles are bytes 0-1 or 2-3 of a panel row
+    const int up_tiles = GLU ? N / 2 / kTileN - 2 : 0;
+    const unsigned up_panels = GLU ? 64u * (unsigned)(N / 2 >> 6) * (unsigned)groups : 0u;
+    const unsigned pvoff2 = pvoff + (unsigned)(nt0 & 2);
     auto w_load = [&](int kt, int part_i, Raw& ws) {  // part_i < kLoads
         const int ktg = kt0 + kt;
         if constexpr (W8) {  // 8-bit layout: 2 KiB tiles, halves 1 KiB apart
@@ -500,8 +585,15 @@ __device__ __forceinline__ void mfma16_body(
             ws.w[cb][u] = buf_load16(
                 w_rsrc, wvoff, (unsigned)(((nt0 + cb) * KTall + ktg) * 2048 + 1024 * u));
         } else if (part_i < 4) {
-            ws.w[part_i] = buf_load16(
-                w_rsrc, wvoff, (unsigned)(((nt0 + part_i) * KTall + ktg) * kTileBytes));
+            const int nt = nt0 + part_i + (GLU && part_i >= 2 ? up_tiles : 0);
+            ws.w[part_i] = buf_load16(w_rsrc, wvoff, (unsigned)((nt * KTall + ktg) * kTileBytes));
+        } else if constexpr (GLU) {
+            const unsigned jo = ppanel + 64u * (unsigned)(ktg * (kTileK / GROUP));
+            const unsigned half = part_i & 1 ? up_panels : 0u;
+            const unsigned short b = __builtin_amdgcn_raw_buffer_load_b16(
+                part_i < 6 ? s_rsrc : a_rsrc, pvoff2, jo + half, 0);
+            if (part_i < 6) ws.sdw[part_i & 1] = b;
+            else ws.adw[part_i & 1] = b;
         } else {
             const unsigned jo = ppanel + 64u * (unsigned)(ktg * (kTileK / GROUP));
             if (part_i == 4) ws.sdw = buf_load4(s_rsrc, pvoff, jo);
@@ -638,6 +730,12 @@ __device__ __forceinline__ void mfma16_body(
                                        reinterpret_cast<unsigned short*>(Y), m0, n0, row_hi, N);
         return;
     }
+    if constexpr (GLU != 0) {
+        sxs[tid % MT] = (m0 + tid % MT < row_hi) ? sx[m0 + tid % MT] : 0.0f;
+        __syncthreads();
+        mfma16_glu_epilogue<MT, GLU>(acc, sxs, sw, ffn, m0, n0, row_hi, N / 2);
+        return;
+    }
     constexpr bool SCALED = (OUT != 1) && !PARTIAL;
     if (SCALED) sxs[tid % MT] = (m0 + tid % MT < row_hi) ? sx[m0 + tid % MT] : 0.0f;
     float swv[4][4];
@@ -755,6 +853,17 @@ __global__ __launch_bounds__(256, MT == 128 ? 2 : 1) void w4a8_mfma16_lora_kerne
     int tiles_n, int tiles_m) {
     mfma16_body<MT, 0, GROUP, false, false, 1, LORA>(X, sx, wq, s_u8, a_u8, sw, Y, nullptr, M, N,
                                                      K, tiles_n, tiles_m, 1, nullptr, lora);
+}
+
+// Gate and up products of a feed-forward block with the activation.
+template <int MT, int GROUP, int GLU>
+__global__ __launch_bounds__(256, MT == 128 ? 2 : 1) void w4a8_mfma16_glu_kernel(
+    const int8_t* __restrict__ X, const float* __restrict__ sx, const uint8_t* __restrict__ wq,
+    const uint8_t* __restrict__ s_u8, const uint8_t* __restrict__ a_u8,
+    const float* __restrict__ sw, FfnOut ffn, int M, int N, int K, int tiles_n, int tiles_m) {
+    mfma16_body<MT, 0, GROUP, false, false, 1, 0, GLU>(X, sx, wq, s_u8, a_u8, sw, nullptr, nullptr,
+                                                       M, N, K, tiles_n, tiles_m, 1, nullptr,
+                                                       LoraArgs{}, ffn);
 }
 
 template <int MT, int OUT, bool PARTIAL, bool W8, int KIN = 1>
@@ -879,6 +988,32 @@ hipError_t launch_w4a8_mfma16_lora(const int8_t* X, const float* sx, const uint8
     }
 #undef T16_LORA_TYPE
 #undef T16_LORA
+    return hipGetLastError();
+}
+
+hipError_t launch_w4a8_mfma16_glu(const int8_t* X, const float* sx, const uint8_t* wq,
+                                  const uint8_t* s_u8, const uint8_t* a_u8, const float* sw,
+                                  int act, float* h, unsigned* tops, int M, int F, int K,
+                                  int group, int mt, hipStream_t st) {
+    const int tiles_n = F / (kNT / 2), tiles_m = (M + mt - 1) / mt;
+    const FfnOut out{h, tops};
+#define T16_GLU(MT_, G_, A_)                                                                      \
+    hipLaunchKernelGGL((w4a8_mfma16_glu_kernel<MT_, G_, A_>), dim3(tiles_n * tiles_m), dim3(256), \
+                       0, st, X, sx, wq, s_u8, a_u8, sw, out, M, 2 * F, K, tiles_n, tiles_m)
+#define T16_GLU_GROUP(MT_, A_)            \
+    do {                                  \
+        if (group == 64) T16_GLU(MT_, 64, A_); \
+        else T16_GLU(MT_, 128, A_);       \
+    } while (0)
+    if (mt == 256) {
+        if (act == 1) T16_GLU_GROUP(256, 2);
+        else T16_GLU_GROUP(256, 1);
+    } else {
+        if (act == 1) T16_GLU_GROUP(128, 2);
+        else T16_GLU_GROUP(128, 1);
+    }
+#undef T16_GLU_GROUP
+#undef T16_GLU
     return hipGetLastError();
 }
 

@@ -177,6 +177,13 @@ hipError_t launch_norm_quant(const NormArgs& a, int x_type, int y_type, hipStrea
 
 // Gated feed-forward block: h = act(gate) up of int32 sums [splits][M][2F]
 // (gate rows first), and its per-row INT8.
+hipError_t launch_w4a8_mfma16_glu(const int8_t* X, const float* sx, const uint8_t* wq,
+                                  const uint8_t* s_u8, const uint8_t* a_u8, const float* sw,
+                                  int act, float* h, unsigned* tops, int M, int F, int K,
+                                  int group, int mt, hipStream_t st);
+// INT8 of h rows whose maxima are those of `ntops` values a row.
+hipError_t launch_ffn_quant(const float* h, const unsigned* tops, int ntops, int M, int F,
+                            int8_t* hq, float* sh, hipStream_t st);
 hipError_t launch_ffn_join(const int* acc, int splits, const float* sx, const float* sw13, int M,
                            int F, int act, int8_t* hq, float* sh, hipStream_t st);
 
