@@ -721,9 +721,16 @@ W4A8_EXPORT w4a8_status_t w4a8_norm_quant(
 
 namespace {
 
+// Streamed gate and up products: pairs of tiles, at least one of each half.
+w4a8::StreamCfg choose_glu_stream(int M, int F, int H) {
+    w4a8::StreamCfg c = choose_stream(M, 2 * F, H, 0, true);
+    if (c.nt_per_wave == 1 || c.nt_per_wave == 7) c.nt_per_wave = 2;
+    return c;
+}
+
 // Workspace of the feed-forward block: the INT8 rows of h and their scales;
 // h itself and its partial maxima, or, where the gate and up products are
-// split over K or streamed, their int32 sums; the down product's own.
+// split over K, their int32 sums; the down product's own.
 struct FfnLayout {
     size_t hq, sh, h, tops, acc, down, bytes;
     bool tiles, down_tiles;
@@ -741,13 +748,14 @@ struct FfnLayout {
         if (tiles) plan = w4a8::plan_w4a8_mfma(M, 2 * F, H);
         down_tiles = use_mfma_tiles(M, H, F);
         if (down_tiles) down_plan = w4a8::plan_w4a8_mfma(M, H, F, true);
-        h = take(fused() ? (size_t)M * F * sizeof(float) : 0);
-        tops = take(fused() ? (size_t)M * (F / 32) * sizeof(unsigned) : 0);
-        acc = take(fused() ? 0 : (size_t)(tiles ? plan.splits : 1) * M * 2 * F * sizeof(int));
+        h = take(split() ? 0 : (size_t)M * F * sizeof(float));
+        tops = take(split() ? 0 : (size_t)M * ntops(F) * sizeof(unsigned));
+        acc = take(split() ? (size_t)plan.splits * M * 2 * F * sizeof(int) : 0);
         down = take(down_plan.workspace);
         bytes = o;
     }
-    bool fused() const { return tiles && plan.splits == 1; }
+    bool split() const { return tiles && plan.splits > 1; }
+    int ntops(int F) const { return tiles ? F / 32 : F / 16; }  // partial maxima of a row
 };
 
 }  // namespace
@@ -784,25 +792,23 @@ W4A8_EXPORT w4a8_status_t w4a8_ffn(const int8_t* Xq, const float* sx, const uint
     int8_t* hq = reinterpret_cast<int8_t*>(ws + lay.hq);
     float* sh = reinterpret_cast<float*>(ws + lay.sh);
     int* acc = reinterpret_cast<int*>(ws + lay.acc);
+    float* h = reinterpret_cast<float*>(ws + lay.h);
+    unsigned* tops = reinterpret_cast<unsigned*>(ws + lay.tops);
     hipError_t e;
-    if (lay.fused()) {
-        float* h = reinterpret_cast<float*>(ws + lay.h);
-        unsigned* tops = reinterpret_cast<unsigned*>(ws + lay.tops);
+    if (lay.split())
+        e = w4a8::launch_w4a8_mfma16_partial(Xq, wq13, s13, a13, M, 2 * F, H, group, lay.plan, acc,
+                                             stream);
+    else if (lay.tiles)
         e = w4a8::launch_w4a8_mfma16_glu(Xq, sx, wq13, s13, a13, sw13, act, h, tops, M, F, H, group,
                                          lay.plan.mt16 ? lay.plan.mt16 : lay.plan.mt, stream);
-        if (e != hipSuccess) return hip_status(e);
-        e = w4a8::launch_ffn_quant(h, tops, F / 32, M, F, hq, sh, stream);
-    } else {
-        if (lay.tiles)
-            e = w4a8::launch_w4a8_mfma16_partial(Xq, wq13, s13, a13, M, 2 * F, H, group, lay.plan,
-                                                 acc, stream);
-        else
-            e = w4a8::launch_w4a8_stream(Xq, sx, wq13, s13, a13, sw13, acc, W4A8_OUT_I32, M, 2 * F,
-                                         H, group, choose_stream(M, 2 * F, H, 0, true), stream);
-        if (e != hipSuccess) return hip_status(e);
-        e = w4a8::launch_ffn_join(acc, lay.tiles ? lay.plan.splits : 1, sx, sw13, M, F, act, hq, sh,
-                                  stream);
-    }
+    else
+        e = w4a8::launch_w4a8_stream_glu(Xq, sx, wq13, s13, a13, sw13, act, h, tops, M, F, H, group,
+                                         choose_glu_stream(M, F, H), stream);
+    if (e != hipSuccess) return hip_status(e);
+    if (lay.split())
+        e = w4a8::launch_ffn_join(acc, lay.plan.splits, sx, sw13, M, F, act, hq, sh, stream);
+    else
+        e = w4a8::launch_ffn_quant(h, tops, lay.ntops(F), M, F, hq, sh, stream);
     if (e != hipSuccess) return hip_status(e);
     const int out = out_type == W4A8_IN_BF16 ? 2 : 0;
     if (lay.down_tiles)

@@ -1,0 +1,71 @@
+// The streamed-tile W4A8 kernel for the gate and up products of a gated
+// feed-forward block (stream_body.h), with the activation in its epilogue.
+#include "stream_body.h"
+
+namespace w4a8 {
+
+template <int NTW, int D, int GROUP, bool LDSP, int RB, int GLU>
+__global__ __launch_bounds__(512) void w4a8_stream_glu_kernel(
+    const int8_t* __restrict__ X, const float* __restrict__ sx, const uint8_t* __restrict__ wq,
+    const uint8_t* __restrict__ s_u8, const uint8_t* __restrict__ a_u8,
+    const float* __restrict__ sw, FfnOut ffn, int M, int N, int K, int ks) {
+    stream_body<NTW, D, 0, GROUP, LDSP, kWkLQQ, RB, 0, GLU>(X, sx, wq, s_u8, a_u8, sw, nullptr, M, N,
+                                                            K, ks, nullptr, nullptr, nullptr,
+                                                            LoraArgs{}, ffn);
+}
+
+namespace {
+
+template <int NTW, int D, int RB>
+hipError_t stream_glu(const int8_t* X, const float* sx, const uint8_t* wq, const uint8_t* s_u8,
+                      const uint8_t* a_u8, const float* sw, int act, const FfnOut& ffn, int M,
+                      int F, int K, int group, int ks, hipStream_t st) {
+    const dim3 grid(F / (kTileN * NTW / 2), (M + 16 * RB - 1) / (16 * RB)), block(64 * ks);
+    const size_t pbytes = (size_t)4 * stream_param_span<NTW / 2>() * (K / group) * 64;
+    const size_t xbytes = (size_t)ks * 2048 * RB;  // X slots
+    const size_t rbytes = (size_t)ks * RB * NTW * 256 * sizeof(int);
+    const bool ldsp = pbytes + xbytes <= 128 * 1024;
+    const size_t used = (ldsp ? pbytes : 0) + xbytes;
+    const size_t lds = used > rbytes ? used : rbytes;
+    if (lds > kMaxLdsBytes) return hipErrorInvalidConfiguration;
+#define GLU_LS(G, P, A)                                                                         \
+    hipLaunchKernelGGL((w4a8_stream_glu_kernel<NTW, D, G, P, RB, A>), grid, block, lds, st, X, \
+                       sx, wq, s_u8, a_u8, sw, ffn, M, 2 * F, K, ks)
+#define GLU_GROUP(P, A)                     \
+    do {                                    \
+        if (group == 64) GLU_LS(64, P, A);  \
+        else GLU_LS(128, P, A);             \
+    } while (0)
+    if (ldsp) {
+        if (act == 1) GLU_GROUP(true, 2);
+        else GLU_GROUP(true, 1);
+    } else {
+        if (act == 1) GLU_GROUP(false, 2);
+        else GLU_GROUP(false, 1);
+    }
+#undef GLU_GROUP
+#undef GLU_LS
+    return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_w4a8_stream_glu(const int8_t* X, const float* sx, const uint8_t* wq,
+                                  const uint8_t* s_u8, const uint8_t* a_u8, const float* sw,
+                                  int act, float* h, unsigned* tops, int M, int F, int K,
+                                  int group, StreamCfg cfg, hipStream_t st) {
+    const FfnOut ffn{h, tops};
+#define GLU_NTW(W, D, R)                                                                       \
+    return stream_glu<W, D, R>(X, sx, wq, s_u8, a_u8, sw, act, ffn, M, F, K, group, cfg.ks, st)
+    switch (cfg.nt_per_wave * 8 + cfg.rb) {
+        case 4 * 8 + 1: GLU_NTW(4, 2, 1);
+        case 4 * 8 + 2: GLU_NTW(4, 2, 2);
+        case 2 * 8 + 1: GLU_NTW(2, 4, 1);
+        case 2 * 8 + 2: GLU_NTW(2, 2, 2);
+        case 2 * 8 + 4: GLU_NTW(2, 2, 4);
+        default: return hipErrorInvalidValue;
+    }
+#undef GLU_NTW
+}
+
+}  // namespace w4a8

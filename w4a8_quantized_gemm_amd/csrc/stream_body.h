@@ -4,6 +4,7 @@
 #include <type_traits>
 
 #include "device_common.h"
+#include "ffn_common.h"
 #include "launch.h"
 #include "lora_common.h"
 
@@ -55,13 +56,17 @@ constexpr int kWkLQQ = 0, kWkW8 = 1, kWkF8 = 2, kWkF8G = 3;
 
 // LORA (1: fp16, 2: bfloat16 adapters; W4A8 to fp16 only): the epilogue adds
 // each row's low-rank adapter to its scaled sums before the one rounding.
-template <int NTW, int D, int OUT, int GROUP, bool LDSP, int WK, int RB, int LORA>
+// GLU (1: SiLU, 2: GELU; W4A8 only): the first half of a workgroup's tiles lie
+// in the gate half of N = 2F, the others are the same ones of the up half, and
+// the epilogue writes act(gate) up with the largest of each row's 16 channels.
+template <int NTW, int D, int OUT, int GROUP, bool LDSP, int WK, int RB, int LORA, int GLU = 0>
 __device__ __forceinline__ void stream_body(
     const int8_t* __restrict__ X, const float* __restrict__ sx, const uint8_t* __restrict__ wq,
     const uint8_t* __restrict__ s_u8, const uint8_t* __restrict__ a_u8,
     const float* __restrict__ sw, void* __restrict__ Y, int M, int N, int K, int ks,
     const int* __restrict__ offsets, const float* __restrict__ fsc,
-    const float* __restrict__ tsc, const LoraArgs& lora) {
+    const float* __restrict__ tsc, const LoraArgs& lora, const FfnOut& ffn = {}) {
+    static_assert(GLU == 0 || (LORA == 0 && WK == kWkLQQ && NTW % 2 == 0), "pairs of tiles");
     static_assert(LORA == 0 || (OUT == 0 && WK == kWkLQQ), "adapters: W4A8 to fp16");
     constexpr bool W8 = WK == kWkW8;
     constexpr bool F8 = WK == kWkF8 || WK == kWkF8G;
@@ -98,7 +103,12 @@ __device__ __forceinline__ void stream_body(
     // XCD (when the group count is a multiple of 8).
     const int nwg = gridDim.x, b = blockIdx.x;
     const int g = (nwg & 7) ? b : (b & 7) * (nwg >> 3) + (b >> 3);
-    const int nt0 = g * NTW;
+    constexpr int NTH = GLU ? NTW / 2 : NTW;  // tiles of one half
+    const int nt0 = g * NTH;
+    // tile t of the workgroup
+    auto tile_of = [&](int t) {
+        return t < NTH ? nt0 + t : N / 2 / kTileN + nt0 + t - NTH;
+    };
     const int nk = (KT - wave + ks - 1) / ks;  // K-tiles of this wave (>= 1: ks <= KT)
     // i-th K-tile of this wave (i < nk)
     auto kt_of = [&](int i) { return wave + ks * i; };
@@ -128,10 +138,12 @@ __device__ __forceinline__ void stream_body(
     // ---- LDS: [parameters (LDSP)] [one 2 KB X slot per wave]; the
     // reduction at the end reuses it from offset 0.
     const int p0 = nt0 >> 2;
-    const int np = ((nt0 + NTW - 1) >> 2) - p0 + 1;
+    const int np = ((nt0 + NTH - 1) >> 2) - p0 + 1;
     uint8_t* lds_s = reinterpret_cast<uint8_t*>(red);
-    uint8_t* lds_a = lds_s + (size_t)np * groups * 64;
-    const int pbytes = LDSP ? 2 * stream_param_span<NTW>() * groups * 64 : 0;
+    // (GLU: the gate half's panels, then the up half's)
+    constexpr int HALVES = GLU ? 2 : 1;
+    uint8_t* lds_a = lds_s + (size_t)HALVES * np * groups * 64;
+    const int pbytes = LDSP ? 2 * HALVES * stream_param_span<NTH>() * groups * 64 : 0;
     uint8_t* xslot = reinterpret_cast<uint8_t*>(red) + pbytes + wave * (2048 * RB);
     // MFMA operand layout: lane (r, G) holds row r, columns 32G .. 32G+31.
     const int xw0 = xpiece(lane >> 3, lane & 7), xw1 = xpiece(8 + (lane >> 3), lane & 7);
@@ -162,12 +174,12 @@ __device__ __forceinline__ void stream_body(
                     st.w[2 * t + u] = __builtin_bit_cast(
                         v4i, __builtin_amdgcn_raw_buffer_load_b128(
                                  w_rsrc, wvoff,
-                                 (unsigned)(((size_t)(nt0 + t) * KT + kt) * 2048 + 1024 * u),
+                                 (unsigned)(((size_t)tile_of(t) * KT + kt) * 2048 + 1024 * u),
                                  kNonTemporal));
             } else {
                 st.w[t] = __builtin_bit_cast(
                     v4i, __builtin_amdgcn_raw_buffer_load_b128(
-                             w_rsrc, wvoff, (unsigned)(((size_t)(nt0 + t) * KT + kt) * kTileBytes),
+                             w_rsrc, wvoff, (unsigned)(((size_t)tile_of(t) * KT + kt) * kTileBytes),
                              kNonTemporal));
             }
             if constexpr (WK == kWkF8G) {
@@ -183,9 +195,10 @@ __device__ __forceinline__ void stream_body(
     };
     auto params = [&](int kt, int t, unsigned& s, unsigned& a) {
         const int j = kt * (kTileK / GROUP) + gsub;
-        const int nt = nt0 + t;
+        const int nt = tile_of(t);
         if (LDSP) {
-            const int o = (((nt >> 2) - p0) * groups + j) * 64 + 4 * r + (nt & 3);
+            const int first = t < NTH ? p0 : (N / 2 >> 6) + p0 - np;
+            const int o = (((nt >> 2) - first) * groups + j) * 64 + 4 * r + (nt & 3);
             s = lds_s[o];
             a = lds_a[o];
         } else {
@@ -279,13 +292,18 @@ __device__ __forceinline__ void stream_body(
     // Parameter copy, behind the first weight loads (panels p0 .. p0+np-1
     // are contiguous in the panel-order arrays).
     if (LDSP && WK == kWkLQQ) {
-        const int n16 = np * groups * 4;  // 16-byte pieces per array
+        const int n16 = np * groups * 4;  // 16-byte pieces per array and half
         const size_t base = (size_t)p0 * groups * 64;
-        for (int q = tid; q < n16; q += blockDim.x) {
-            const v4i vs = *reinterpret_cast<const v4i*>(s_u8 + base + (size_t)q * 16);
-            const v4i va = *reinterpret_cast<const v4i*>(a_u8 + base + (size_t)q * 16);
-            *reinterpret_cast<v4i*>(lds_s + q * 16) = vs;
-            *reinterpret_cast<v4i*>(lds_a + q * 16) = va;
+#pragma unroll
+        for (int hf = 0; hf < HALVES; ++hf) {
+            const size_t from = base + (size_t)hf * (N / 2 >> 6) * groups * 64;
+            const int to = hf * n16 * 16;
+            for (int q = tid; q < n16; q += blockDim.x) {
+                const v4i vs = *reinterpret_cast<const v4i*>(s_u8 + from + (size_t)q * 16);
+                const v4i va = *reinterpret_cast<const v4i*>(a_u8 + from + (size_t)q * 16);
+                *reinterpret_cast<v4i*>(lds_s + to + q * 16) = vs;
+                *reinterpret_cast<v4i*>(lds_a + to + q * 16) = va;
+            }
         }
         __syncthreads();
     }
@@ -364,6 +382,31 @@ __device__ __forceinline__ void stream_body(
             *reinterpret_cast<uint2*>(reinterpret_cast<unsigned short*>(Y) + (size_t)m * N + n +
                                       4 * G) =
                 uint2{h[0] | ((unsigned)h[1] << 16), h[2] | ((unsigned)h[3] << 16)};
+        }
+        return;
+    }
+    if constexpr (GLU != 0) {
+        // a wave's 64 elements are four rows of 16 channels of one tile pair
+        constexpr int NPAIR = RB * NTH * 256;
+        const int F = N / 2;
+        for (int q = tid; q < NPAIR; q += blockDim.x) {
+            const int rb = q / (NTH * 256), t = (q >> 8) % NTH, v = (q >> 6) & 3, l = q & 63;
+            const int e = rb * (NTW * 256) + t * 256 + (q & 255);
+            int sum[2] = {0, 0};
+            for (int w = 0; w < ks; ++w) {
+                sum[0] += red[w * (RB * NTW * 256) + e];
+                sum[1] += red[w * (RB * NTW * 256) + NTH * 256 + e];
+            }
+            const int m = m0 + 16 * rb + 4 * (l >> 4) + v;
+            const int n = (nt0 + t) * kTileN + (l & 15);
+            const bool on = m < row_hi;
+            const float x = on ? sx[m] : 0.0f;
+            const float h =
+                gated<GLU - 1>(((float)sum[0] * x) * sw[n], ((float)sum[1] * x) * sw[F + n]);
+            const unsigned top = row16_reduce(abs_bits(h), MaxU32{});
+            if (!on) continue;
+            ffn.h[(size_t)m * F + n] = h;
+            if ((l & 15) == 0) ffn.tops[(size_t)m * (F / 16) + n / 16] = top;
         }
         return;
     }
