@@ -721,41 +721,121 @@ W4A8_EXPORT w4a8_status_t w4a8_norm_quant(
 
 namespace {
 
-// Streamed gate and up products: pairs of tiles, at least one of each half.
-w4a8::StreamCfg choose_glu_stream(int M, int F, int H) {
-    w4a8::StreamCfg c = choose_stream(M, 2 * F, H, 0, true);
-    if (c.nt_per_wave == 1 || c.nt_per_wave == 7) c.nt_per_wave = 2;
-    return c;
-}
+// Kernels of the feed-forward block.  us measured on 4096 x 11008 (A), 8192 x
+// 28672 (B), 4096 x 6400 (C) and 2048 x 1408 (D) blocks (H x F).
+struct FfnPlan {
+    bool up_stream, down_stream, down64;
+    w4a8::StreamCfg up{}, down{};
+    int up_mt = 0, up_kin = 1;
+    w4a8::MfmaPlan down_plan{};
+    int down_splits = 1;
+    size_t down_bytes = 0;  // int32 partials of the down product
 
-// Workspace of the feed-forward block: the INT8 rows of h and their scales;
-// h itself and its partial maxima, or, where the gate and up products are
-// split over K, their int32 sums; the down product's own.
+    FfnPlan(int M, int H, int F) {
+        plan_up(M, H, F);
+        plan_down(M, H, F);
+    }
+
+    // Gate and up.  Streamed up to 32 rows, and while workgroups of 64 rows and
+    // 64 channels of each half would leave half of the CUs without one (D, 133
+    // rows: 7.6 against 11 or more; C, 64 rows: 16 against 17.9, 96 rows: 21.4
+    // against 17.8).
+    void plan_up(int M, int H, int F) {
+        const long long t64 = (long long)(F / 64) * ((M + 63) / 64);
+        up_stream = M <= 32 || t64 < 128;
+        if (up_stream) {
+            // Row blocks: two from 17 rows on.  Four tiles (two of each half)
+            // where that leaves workgroups enough, else two: one block, B 42.2 /
+            // 44.0 at 16 rows and 41.9 / 40.6 at one, A 14.5 / 12.6; two blocks, B
+            // 46.3 / 48.0 at 17 rows, C 15.3 / 17.3 at 47, A 16.2 / 14.1 at 17.
+            up.rb = M <= 16 ? 1 : 2;
+            const long long wide = (long long)(F / 32) * ((M + 16 * up.rb - 1) / (16 * up.rb));
+            up.nt_per_wave = wide >= (up.rb == 1 ? 768 : 400) ? 4 : 2;
+            // Waves splitting K: four; eight for few workgroups (D, 17 rows: 5.7 /
+            // 6.5), two for very many (D, 300 rows: 10.1 / 12.3).
+            const long long wgs = up.nt_per_wave == 4 ? wide : 2 * wide;
+            up.ks = wgs <= 352 ? 8 : (M > 64 && wgs > 640) ? 2 : 4;
+            while (up.ks > 1 && k_tiles(H) < up.ks) up.ks /= 2;
+            return;
+        }
+        // Tiles: the GEMM's height where its workgroups (128 channels of each
+        // half) cover most CUs; else 64 rows, 64 channels of each half and two K
+        // parts (A, 64 rows: 19.6 against 33; C, 200 rows: 24.5 against 33.7).
+        // Just past one workgroup per CU a second round would be nearly empty:
+        // 64 rows (A, 300 rows: 45.9 against 53.8).
+        const w4a8::MfmaPlan p = w4a8::plan_w4a8_mfma(M, 2 * F, H);
+        up_mt = p.mt16 ? p.mt16 : p.mt;
+        const long long wgs = (long long)(F / 128) * ((M + up_mt - 1) / up_mt);
+        if (M <= 64 || wgs < 160) {
+            up_mt = 64;
+            up_kin = 2;
+        } else if (up_mt == 128 && wgs > 256 && wgs <= 320) {
+            up_mt = 64;
+        }
+    }
+
+    // Down.  Streamed with two tiles and up to two row blocks while its
+    // workgroups read few activations again (M N K of 2^31.6: A up to 64 rows 14.3
+    // against 15.3, D up to 300 rows 7.9 against 7.9, C at 96 rows 13.0 against
+    // 14.5; B, 47 rows: 39 against 31.4), and up to 32 rows (B, 32 rows: 30.5
+    // against 29.7; 17 rows: 25.8 against 29.0).
+    void plan_down(int M, int H, int F) {
+        const long long t64 = (long long)(H / 128) * ((M + 63) / 64);
+        const double work = (double)M * H * F;
+        down64 = false;
+        down_stream = M <= 32 || (t64 < 128 && work <= 3.2e9);
+        if (down_stream) {
+            down = choose_stream(M, H, F, 0, true);
+            if (M > 32) {
+                down.nt_per_wave = 2;
+                down.rb = 2;
+                const long long wgs = (long long)(H / 32) * ((M + 31) / 32);
+                down.ks = wgs <= 256 ? 8 : 4;
+                while (down.ks > 1 && k_tiles(F) < down.ks) down.ks /= 2;
+            }
+            return;
+        }
+        // 64-row tiles of 128 channels in two K parts, K split further to fill
+        // two workgroups per CU: up to 64 rows (B: 33.6 against 36.5), and for
+        // medium blocks (A, 96 rows: 18.0 against 18.6, 300 rows: 27.1 against 28.0;
+        // C, 200 rows: 17.9 against 20.3; B, 96 rows: 42.8 against 38.8).
+        // And where the GEMM's 256-channel tiles do not divide H.
+        down64 = M <= 64 || (t64 <= 256 && work <= 16e9) || !use_mfma_tiles(M, H, F);
+        if (down64) {
+            int s = (int)(512 / t64);
+            const int most = M <= 64 ? 8 : 4;
+            if (s > most) s = most;
+            while (s > 1 && k_tiles(F) < 20 * s) --s;
+            down_splits = s < 1 ? 1 : s;
+            down_bytes = down_splits > 1 ? (size_t)down_splits * M * H * sizeof(int) : 0;
+            return;
+        }
+        down_plan = w4a8::plan_w4a8_mfma(M, H, F, true);
+        down_bytes = down_plan.workspace;
+    }
+};
+
+// Workspace of the feed-forward block: the INT8 rows of h and their scales, h
+// and the maxima of its parts, the down product's partial sums.
 struct FfnLayout {
-    size_t hq, sh, h, tops, acc, down, bytes;
-    bool tiles, down_tiles;
-    w4a8::MfmaPlan plan{}, down_plan{};
-    FfnLayout(int M, int H, int F) {
+    FfnPlan plan;
+    size_t hq, sh, h, tops, down, bytes;
+    int ntops;  // partial maxima of a row
+    FfnLayout(int M, int H, int F) : plan(M, H, F) {
         size_t o = 0;
         auto take = [&](size_t n) {
             const size_t at = o;
             o += (n + 255) & ~(size_t)255;
             return at;
         };
+        ntops = plan.up_stream ? F / 16 : F / 32;
         hq = take((size_t)M * F);
         sh = take((size_t)M * sizeof(float));
-        tiles = use_mfma_tiles(M, 2 * F, H);
-        if (tiles) plan = w4a8::plan_w4a8_mfma(M, 2 * F, H);
-        down_tiles = use_mfma_tiles(M, H, F);
-        if (down_tiles) down_plan = w4a8::plan_w4a8_mfma(M, H, F, true);
-        h = take(split() ? 0 : (size_t)M * F * sizeof(float));
-        tops = take(split() ? 0 : (size_t)M * ntops(F) * sizeof(unsigned));
-        acc = take(split() ? (size_t)plan.splits * M * 2 * F * sizeof(int) : 0);
-        down = take(down_plan.workspace);
+        h = take((size_t)M * F * sizeof(float));
+        tops = take((size_t)M * ntops * sizeof(unsigned));
+        down = take(plan.down_bytes);
         bytes = o;
     }
-    bool split() const { return tiles && plan.splits > 1; }
-    int ntops(int F) const { return tiles ? F / 32 : F / 16; }  // partial maxima of a row
 };
 
 }  // namespace
@@ -791,29 +871,25 @@ W4A8_EXPORT w4a8_status_t w4a8_ffn(const int8_t* Xq, const float* sx, const uint
     uint8_t* ws = reinterpret_cast<uint8_t*>(workspace);
     int8_t* hq = reinterpret_cast<int8_t*>(ws + lay.hq);
     float* sh = reinterpret_cast<float*>(ws + lay.sh);
-    int* acc = reinterpret_cast<int*>(ws + lay.acc);
     float* h = reinterpret_cast<float*>(ws + lay.h);
     unsigned* tops = reinterpret_cast<unsigned*>(ws + lay.tops);
-    hipError_t e;
-    if (lay.split())
-        e = w4a8::launch_w4a8_mfma16_partial(Xq, wq13, s13, a13, M, 2 * F, H, group, lay.plan, acc,
-                                             stream);
-    else if (lay.tiles)
-        e = w4a8::launch_w4a8_mfma16_glu(Xq, sx, wq13, s13, a13, sw13, act, h, tops, M, F, H, group,
-                                         lay.plan.mt16 ? lay.plan.mt16 : lay.plan.mt, stream);
-    else
-        e = w4a8::launch_w4a8_stream_glu(Xq, sx, wq13, s13, a13, sw13, act, h, tops, M, F, H, group,
-                                         choose_glu_stream(M, F, H), stream);
+    const FfnPlan& p = lay.plan;
+    hipError_t e =
+        p.up_stream ? w4a8::launch_w4a8_stream_glu(Xq, sx, wq13, s13, a13, sw13, act, h, tops, M, F,
+                                                   H, group, p.up, stream)
+                    : w4a8::launch_w4a8_ffn_up(Xq, sx, wq13, s13, a13, sw13, act, h, tops, M, F, H,
+                                               group, p.up_mt, p.up_kin, stream);
     if (e != hipSuccess) return hip_status(e);
-    if (lay.split())
-        e = w4a8::launch_ffn_join(acc, lay.plan.splits, sx, sw13, M, F, act, hq, sh, stream);
-    else
-        e = w4a8::launch_ffn_quant(h, tops, lay.ntops(F), M, F, hq, sh, stream);
+    e = w4a8::launch_ffn_quant(h, tops, lay.ntops, M, F, hq, sh, stream);
     if (e != hipSuccess) return hip_status(e);
     const int out = out_type == W4A8_IN_BF16 ? 2 : 0;
-    if (lay.down_tiles)
-        return hip_status(w4a8::launch_w4a8_mfma(hq, sh, wq2, s2, a2, sw2, Y, out, M, H, F, group,
-                                                 lay.down_plan, ws + lay.down, stream));
-    return hip_status(w4a8::launch_w4a8_stream(hq, sh, wq2, s2, a2, sw2, Y, out, M, H, F, group,
-                                               choose_stream(M, H, F, 0, true), stream));
+    if (p.down_stream)
+        return hip_status(w4a8::launch_w4a8_stream(hq, sh, wq2, s2, a2, sw2, Y, out, M, H, F, group,
+                                                   p.down, stream));
+    if (p.down64)
+        return hip_status(w4a8::launch_w4a8_ffn_down64(
+            hq, sh, wq2, s2, a2, sw2, Y, out, M, H, F, group, p.down_splits,
+            reinterpret_cast<int*>(ws + lay.down), stream));
+    return hip_status(w4a8::launch_w4a8_mfma(hq, sh, wq2, s2, a2, sw2, Y, out, M, H, F, group,
+                                             p.down_plan, ws + lay.down, stream));
 }

@@ -175,12 +175,13 @@ struct NormArgs {
 };
 hipError_t launch_norm_quant(const NormArgs& a, int x_type, int y_type, hipStream_t st);
 
-// Gated feed-forward block: h = act(gate) up of int32 sums [splits][M][2F]
-// (gate rows first), and its per-row INT8.
-hipError_t launch_w4a8_mfma16_glu(const int8_t* X, const float* sx, const uint8_t* wq,
-                                  const uint8_t* s_u8, const uint8_t* a_u8, const float* sw,
-                                  int act, float* h, unsigned* tops, int M, int F, int K,
-                                  int group, int mt, hipStream_t st);
+// Gated feed-forward block.  The gate and up products of W13 [2F][K] with the
+// activation: h [M][F], and the maxima of every 32 (tile kernel of mt = 64, 128
+// or 256 rows, kin K parts of 64-row tiles) or 16 (streamed) channels of a row.
+hipError_t launch_w4a8_ffn_up(const int8_t* X, const float* sx, const uint8_t* wq,
+                              const uint8_t* s_u8, const uint8_t* a_u8, const float* sw, int act,
+                              float* h, unsigned* tops, int M, int F, int K, int group, int mt,
+                              int kin, hipStream_t st);
 hipError_t launch_w4a8_stream_glu(const int8_t* X, const float* sx, const uint8_t* wq,
                                   const uint8_t* s_u8, const uint8_t* a_u8, const float* sw,
                                   int act, float* h, unsigned* tops, int M, int F, int K,
@@ -188,8 +189,12 @@ hipError_t launch_w4a8_stream_glu(const int8_t* X, const float* sx, const uint8_
 // INT8 of h rows whose maxima are those of `ntops` values a row.
 hipError_t launch_ffn_quant(const float* h, const unsigned* tops, int ntops, int M, int F,
                             int8_t* hq, float* sh, hipStream_t st);
-hipError_t launch_ffn_join(const int* acc, int splits, const float* sx, const float* sw13, int M,
-                           int F, int act, int8_t* hq, float* sh, hipStream_t st);
+// The down product on 64-row tiles with two K parts (N % 128 == 0; splits > 1:
+// int32 partials in `part`).
+hipError_t launch_w4a8_ffn_down64(const int8_t* X, const float* sx, const uint8_t* wq,
+                                  const uint8_t* s_u8, const uint8_t* a_u8, const float* sw,
+                                  void* Y, int out_type, int M, int N, int K, int group, int splits,
+                                  int* part, hipStream_t st);
 
 // Low-rank adapters: V [M][R] float32 = scale (X . A^T) of the rows that
 // select one, B [n_adapters][N][R] of in_type.
