@@ -330,6 +330,17 @@ FFN = [
     (1, 4096, 1408, 128, "gelu", "bf16"),
     (1, 256, 11008, 64, "silu", "f16"),
     (2, 384, 640, 128, "silu", "bf16"),
+    # up to four rows are quantised by the down product's workgroups
+    (3, 1152, 384, 64, "silu", "f16"),
+    (4, 4096, 1408, 128, "gelu", "bf16"),
+    (4, 8192, 5504, 64, "silu", "bf16"),
+    (5, 1152, 384, 64, "silu", "f16"),
+    # group parameters of the longest rows do not fit in LDS
+    (2, 128, 131072, 64, "silu", "bf16"),
+    (20, 128, 131072, 64, "silu", "f16"),
+    (70, 128, 131072, 128, "gelu", "f16"),
+    (3, 131072, 128, 64, "silu", "f16"),
+    (40, 131072, 128, 64, "gelu", "bf16"),
     (15, 512, 384, 64, "gelu", "f16"),
     (16, 1024, 2688, 128, "silu", "bf16"),
     (17, 640, 896, 64, "silu", "f16"),

@@ -483,6 +483,10 @@ try:  # the current stream of a device as an integer, without a Stream object
 except ImportError:
     def _raw_stream(index):
         return torch.cuda.current_stream(index).cuda_stream
+try:  # the current device, for code that already holds a tensor on one
+    from torch._C import _cuda_getDevice as _current_device
+except ImportError:
+    _current_device = torch.cuda.current_device
 
 
 def _ready(t, dtype, shape, device, name):
@@ -540,7 +544,7 @@ def _context(device, stream):
         if stream.device != device:
             raise ValueError(f"stream is on {stream.device}, the tensors on {device}")
         return torch.cuda.stream(stream)
-    if torch.cuda.current_device() != device.index:
+    if _current_device() != device.index:
         return torch.cuda.device(device)
     return _HERE
 
@@ -567,6 +571,26 @@ def _packed_ready(p, keys, E, device, name):
     for k in keys:
         _ready(p[k], torch.float32 if k == "sw" else torch.uint8, (E * sizes[k],), device,
                f"{name}[{k!r}]")
+
+
+def _packed_ptrs(p, device, name):
+    """Addresses of one matrix's packed arrays, checked as _ready does."""
+    wq, s, a, sw = p["wq"], p["s_u8"], p["a_u8"], p["sw"]
+    N, i = p["N"], device.index
+    n = N * p["K"]
+    try:
+        if (wq.numel() * 2 == n and wq.dtype is torch.uint8 and wq.get_device() == i
+                and wq.is_contiguous() and sw.numel() == N and sw.dtype is torch.float32
+                and sw.get_device() == i and sw.is_contiguous()):
+            n //= p["group"]
+            if (s.numel() == n and s.dtype is torch.uint8 and s.get_device() == i
+                    and s.is_contiguous() and a.numel() == n and a.dtype is torch.uint8
+                    and a.get_device() == i and a.is_contiguous()):
+                return wq.data_ptr(), s.data_ptr(), a.data_ptr(), sw.data_ptr()
+    except AttributeError:
+        pass
+    _packed_ready(p, ("wq", "s_u8", "a_u8", "sw"), 1, device, name)
+    raise ValueError(f"the packed arrays of {name} must be 1-D")
 
 
 def route_workspace_size(T: int, E: int, k: int) -> int:
@@ -703,14 +727,6 @@ _NORM_OUT_DTYPE = {NORM_OUT_F32: torch.float32, NORM_OUT_F16: torch.float16,
                    NORM_OUT_E4M3: torch.uint8}
 
 
-def _opt(t, dtype, shape, device, name):
-    """Address of an optional tensor, checked."""
-    if t is None:
-        return None
-    _ready(t, dtype, shape, device, name)
-    return t.data_ptr()
-
-
 def norm_quant(x, weight=None, bias=None, y=None, y_weight=None, y_bias=None, gate=None,
                gate_ids=None, x_scale: float = 1.0, y_scale: float = 1.0, eps: float = 1e-5,
                kind: int = NORM_RMS, out_type: int = NORM_OUT_INT8, out=None, stream=None):
@@ -730,18 +746,19 @@ def norm_quant(x, weight=None, bias=None, y=None, y_weight=None, y_bias=None, ga
     without y).  `out`: such a dict to write into; its x may be the input x."""
     xt = _float_type(x, "x")
     _on_gpu(x, "x")
-    M, K = x.shape
+    M, K = shape = x.shape
     dev = x.device
-    _ready(x, x.dtype, (M, K), dev, "x")
+    if not x.is_contiguous():
+        _not_ready(x, x.dtype, shape, dev, "x")
     dtype = _NORM_OUT_DTYPE.get(out_type)
     if dtype is None:
         raise ValueError(f"out_type must be one of the NORM_OUT_ constants, got {out_type}")
     quantised = out_type >= NORM_OUT_INT8
     yt = rows = 0
-    y_ptr = gate_ptr = ids_ptr = None
+    y_ptr = gate_ptr = ids_ptr = w_ptr = b_ptr = yw_ptr = yb_ptr = x_ptr = None
     if y is not None:
         yt = _float_type(y, "y")
-        _ready(y, y.dtype, (M, K), dev, "y")
+        _ready(y, y.dtype, shape, dev, "y")
         y_ptr = y.data_ptr()
         if gate is not None:
             if not isinstance(gate, torch.Tensor) or gate.dim() != 2:
@@ -751,32 +768,51 @@ def norm_quant(x, weight=None, bias=None, y=None, y_weight=None, y_bias=None, ga
                 raise ValueError(f"gate must have 1 or {M} rows, or gate_ids; got {rows}")
             _ready(gate, y.dtype, (rows, K), dev, "gate")
             gate_ptr = gate.data_ptr()
-            ids_ptr = _opt(gate_ids, torch.int32, (M,), dev, "gate_ids")
+            if gate_ids is not None:
+                _ready(gate_ids, torch.int32, (M,), dev, "gate_ids")
+                ids_ptr = gate_ids.data_ptr()
         elif gate_ids is not None:
             raise ValueError("gate_ids needs a gate")
-    elif y_weight is not None or gate is not None or gate_ids is not None:
-        raise ValueError("y_weight, gate and gate_ids need y")
-    if (bias is not None and weight is None) or (y_bias is not None and y_weight is None):
+        if y_weight is not None:
+            _ready(y_weight, torch.float32, (K,), dev, "y_weight")
+            yw_ptr = y_weight.data_ptr()
+            if y_bias is not None:
+                _ready(y_bias, torch.float32, (K,), dev, "y_bias")
+                yb_ptr = y_bias.data_ptr()
+        elif y_bias is not None:
+            raise ValueError("a bias needs its weight")
+    elif y_weight is not None or y_bias is not None or gate is not None or gate_ids is not None:
+        raise ValueError("y_weight, y_bias, gate and gate_ids need y")
+    if weight is not None:
+        _ready(weight, torch.float32, (K,), dev, "weight")
+        w_ptr = weight.data_ptr()
+        if bias is not None:
+            _ready(bias, torch.float32, (K,), dev, "bias")
+            b_ptr = bias.data_ptr()
+    elif bias is not None:
         raise ValueError("a bias needs its weight")
     with _context(dev, stream):
         if out is None:
-            out = {"out": torch.empty((M, K), dtype=dtype, device=dev),
+            out = {"out": torch.empty(shape, dtype=dtype, device=dev),
                    "sx": torch.empty(M, dtype=torch.float32, device=dev) if quantised else None,
-                   "x": x if y is None else torch.empty((M, K), dtype=x.dtype, device=dev)}
+                   "x": x if y is None else torch.empty(shape, dtype=x.dtype, device=dev)}
+            dst = out["out"]
         else:
-            _ready(out["out"], dtype, (M, K), dev, "out['out']")
+            dst = out["out"]
+            _ready(dst, dtype, shape, dev, "out['out']")
             if quantised:
                 _ready(out["sx"], torch.float32, (M,), dev, "out['sx']")
             if y is not None:
-                _ready(out["x"], x.dtype, (M, K), dev, "out['x']")
-        _check(lib.w4a8_norm_quant(
-            x.data_ptr(), xt, y_ptr, yt, _opt(y_weight, torch.float32, (K,), dev, "y_weight"),
-            _opt(y_bias, torch.float32, (K,), dev, "y_bias"), gate_ptr, rows, ids_ptr, x_scale,
-            y_scale, _opt(weight, torch.float32, (K,), dev, "weight"),
-            _opt(bias, torch.float32, (K,), dev, "bias"), kind, eps,
-            None if y is None else out["x"].data_ptr(), out["out"].data_ptr(), out_type,
-            out["sx"].data_ptr() if quantised else None, M, K, _raw_stream(dev.index)),
-            "w4a8_norm_quant")
+                _ready(out["x"], x.dtype, shape, dev, "out['x']")
+        if y is not None:
+            x_ptr = out["x"].data_ptr()
+        status = lib.w4a8_norm_quant(x.data_ptr(), xt, y_ptr, yt, yw_ptr, yb_ptr, gate_ptr, rows,
+                                     ids_ptr, x_scale, y_scale, w_ptr, b_ptr, kind, eps, x_ptr,
+                                     dst.data_ptr(), out_type,
+                                     out["sx"].data_ptr() if quantised else None, M, K,
+                                     _raw_stream(dev.index))
+    if status:
+        _check(status, "w4a8_norm_quant")
     return out
 
 
@@ -805,17 +841,15 @@ def ffn(Xq, sx, w13, w2, act: int = ACT_SILU, dtype=torch.float16, out=None, wor
                          f"[{w13['N']}][{w13['K']}] and [{w2['N']}][{w2['K']}]")
     _ready(Xq, torch.int8, (M, H), dev, "Xq")
     _ready(sx, torch.float32, (M,), dev, "sx")
-    for p, name in ((w13, "w13"), (w2, "w2")):
-        _packed_ready(p, ("wq", "s_u8", "a_u8", "sw"), 1, dev, name)
+    p13, p2 = _packed_ptrs(w13, dev, "w13"), _packed_ptrs(w2, dev, "w2")
     with _context(dev, stream):
         if out is None:
             out = torch.empty((M, H), dtype=dtype, device=dev)
         ot = _float_type(out, "out", _HALF_TYPES)
         _ready(out, out.dtype, (M, H), dev, "out")
         ws, ws_ptr, ws_bytes = _workspace(workspace, ffn_workspace_size, (M, H, F), dev)
-        _check(lib.w4a8_ffn(Xq.data_ptr(), sx.data_ptr(), w13["wq"].data_ptr(),
-                            w13["s_u8"].data_ptr(), w13["a_u8"].data_ptr(), w13["sw"].data_ptr(),
-                            w2["wq"].data_ptr(), w2["s_u8"].data_ptr(), w2["a_u8"].data_ptr(),
-                            w2["sw"].data_ptr(), act, out.data_ptr(), ot, M, H, F, g, ws_ptr,
-                            ws_bytes, _raw_stream(dev.index)), "w4a8_ffn")
+        status = lib.w4a8_ffn(Xq.data_ptr(), sx.data_ptr(), *p13, *p2, act, out.data_ptr(), ot, M, H,
+                              F, g, ws_ptr, ws_bytes, _raw_stream(dev.index))
+    if status:
+        _check(status, "w4a8_ffn")
     return out

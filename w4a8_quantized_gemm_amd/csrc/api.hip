@@ -725,6 +725,7 @@ namespace {
 // 28672 (B), 4096 x 6400 (C) and 2048 x 1408 (D) blocks (H x F).
 struct FfnPlan {
     bool up_stream, down_stream, down64;
+    bool down_rows = false;  // h quantised by the down product's workgroups
     w4a8::StreamCfg up{}, down{};
     int up_mt = 0, up_kin = 1;
     w4a8::MfmaPlan down_plan{};
@@ -750,7 +751,7 @@ struct FfnPlan {
             // 46.3 / 48.0 at 17 rows, C 15.3 / 17.3 at 47, A 16.2 / 14.1 at 17.
             up.rb = M <= 16 ? 1 : 2;
             const long long wide = (long long)(F / 32) * ((M + 16 * up.rb - 1) / (16 * up.rb));
-            up.nt_per_wave = wide >= (up.rb == 1 ? 768 : 400) ? 4 : 2;
+            up.nt_per_wave = M > 1 && wide >= (up.rb == 1 ? 768 : 400) ? 4 : 2;
             // Waves splitting K: four; eight for few workgroups (D, 17 rows: 5.7 /
             // 6.5), two for very many (D, 300 rows: 10.1 / 12.3).
             const long long wgs = up.nt_per_wave == 4 ? wide : 2 * wide;
@@ -786,6 +787,8 @@ struct FfnPlan {
         down_stream = M <= 32 || (t64 < 128 && work <= 3.2e9);
         if (down_stream) {
             down = choose_stream(M, H, F, 0, true);
+            down_rows = M <= w4a8::kFewRows;
+            if (down_rows && down.nt_per_wave > 2) down.nt_per_wave = 2;
             if (M > 32) {
                 down.nt_per_wave = 2;
                 down.rb = 2;
@@ -880,9 +883,12 @@ W4A8_EXPORT w4a8_status_t w4a8_ffn(const int8_t* Xq, const float* sx, const uint
                     : w4a8::launch_w4a8_ffn_up(Xq, sx, wq13, s13, a13, sw13, act, h, tops, M, F, H,
                                                group, p.up_mt, p.up_kin, stream);
     if (e != hipSuccess) return hip_status(e);
+    const int out = out_type == W4A8_IN_BF16 ? 2 : 0;
+    if (p.down_rows)
+        return hip_status(w4a8::launch_w4a8_stream_rows(h, tops, lay.ntops, wq2, s2, a2, sw2, Y, out,
+                                                        M, H, F, group, p.down, stream));
     e = w4a8::launch_ffn_quant(h, tops, lay.ntops, M, F, hq, sh, stream);
     if (e != hipSuccess) return hip_status(e);
-    const int out = out_type == W4A8_IN_BF16 ? 2 : 0;
     if (p.down_stream)
         return hip_status(w4a8::launch_w4a8_stream(hq, sh, wq2, s2, a2, sw2, Y, out, M, H, F, group,
                                                    p.down, stream));

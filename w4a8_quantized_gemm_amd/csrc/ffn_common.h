@@ -22,9 +22,10 @@ __device__ __forceinline__ float gated(float g, float u) {
 // 16 (streamed) or 32 (tile) channels as the bits of a float: the row's
 // maximum is known without reading h again, and no workgroup waits for
 // another's atomic.
-struct FfnOut {
+struct FfnRows {
     float* h;         // [M][F]
-    unsigned* tops;   // [M][F / 16] or [M][F / 32]
+    unsigned* tops;   // [M][ntops]
+    int ntops;        // F / 16 or F / 32
 };
 
 }  // namespace w4a8

@@ -9,7 +9,7 @@ template <int MT, int GROUP, int KIN, int GLU>
 __global__ __launch_bounds__(256, MT <= 128 ? 2 : 1) void w4a8_ffn_up_kernel(
     const int8_t* __restrict__ X, const float* __restrict__ sx, const uint8_t* __restrict__ wq,
     const uint8_t* __restrict__ s_u8, const uint8_t* __restrict__ a_u8,
-    const float* __restrict__ sw, FfnOut ffn, int M, int N, int K, int tiles_n, int tiles_m) {
+    const float* __restrict__ sw, FfnRows ffn, int M, int N, int K, int tiles_n, int tiles_m) {
     mfma16_body<MT, 0, GROUP, false, false, KIN, 0, GLU>(X, sx, wq, s_u8, a_u8, sw, nullptr,
                                                          nullptr, M, N, K, tiles_n, tiles_m, 1,
                                                          nullptr, LoraArgs{}, ffn);
@@ -31,7 +31,7 @@ namespace {
 
 template <int MT, int KIN>
 void launch_up(const int8_t* X, const float* sx, const uint8_t* wq, const uint8_t* s_u8,
-               const uint8_t* a_u8, const float* sw, int act, const FfnOut& out, int M, int F,
+               const uint8_t* a_u8, const float* sw, int act, const FfnRows& out, int M, int F,
                int K, int group, hipStream_t st) {
     const int tiles_n = F / (kNT / 2 / KIN), tiles_m = (M + MT - 1) / MT;
 #define UP(G_, A_)                                                                          \
@@ -68,7 +68,7 @@ hipError_t launch_w4a8_ffn_up(const int8_t* X, const float* sx, const uint8_t* w
                               const uint8_t* s_u8, const uint8_t* a_u8, const float* sw, int act,
                               float* h, unsigned* tops, int M, int F, int K, int group, int mt,
                               int kin, hipStream_t st) {
-    const FfnOut out{h, tops};
+    const FfnRows out{h, tops, F / 32};
     if (mt == 256) launch_up<256, 1>(X, sx, wq, s_u8, a_u8, sw, act, out, M, F, K, group, st);
     else if (mt == 128) launch_up<128, 1>(X, sx, wq, s_u8, a_u8, sw, act, out, M, F, K, group, st);
     else if (kin == 1) launch_up<64, 1>(X, sx, wq, s_u8, a_u8, sw, act, out, M, F, K, group, st);

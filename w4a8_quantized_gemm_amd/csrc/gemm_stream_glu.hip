@@ -1,5 +1,6 @@
-// The streamed-tile W4A8 kernel for the gate and up products of a gated
-// feed-forward block (stream_body.h), with the activation in its epilogue.
+// The streamed-tile W4A8 kernel (stream_body.h) for a gated feed-forward block:
+// its gate and up products with the activation in the epilogue, and the down
+// product of a few rows that its workgroups quantise themselves.
 #include "stream_body.h"
 
 namespace w4a8 {
@@ -8,17 +9,58 @@ template <int NTW, int D, int GROUP, bool LDSP, int RB, int GLU>
 __global__ __launch_bounds__(512) void w4a8_stream_glu_kernel(
     const int8_t* __restrict__ X, const float* __restrict__ sx, const uint8_t* __restrict__ wq,
     const uint8_t* __restrict__ s_u8, const uint8_t* __restrict__ a_u8,
-    const float* __restrict__ sw, FfnOut ffn, int M, int N, int K, int ks) {
+    const float* __restrict__ sw, FfnRows ffn, int M, int N, int K, int ks) {
     stream_body<NTW, D, 0, GROUP, LDSP, kWkLQQ, RB, 0, GLU>(X, sx, wq, s_u8, a_u8, sw, nullptr, M, N,
                                                             K, ks, nullptr, nullptr, nullptr,
                                                             LoraArgs{}, ffn);
 }
 
+template <int NTW, int D, int OUT, int GROUP, bool LDSP, int ROWS>
+__global__ __launch_bounds__(512) void w4a8_stream_rows_kernel(
+    FfnRows ffn, const uint8_t* __restrict__ wq, const uint8_t* __restrict__ s_u8,
+    const uint8_t* __restrict__ a_u8, const float* __restrict__ sw, void* __restrict__ Y, int N,
+    int K, int ks) {
+    stream_body<NTW, D, OUT, GROUP, LDSP, kWkLQQ, 1, 0, 0, ROWS>(
+        nullptr, nullptr, wq, s_u8, a_u8, sw, Y, ROWS, N, K, ks, nullptr, nullptr, nullptr, LoraArgs{},
+        ffn);
+}
+
 namespace {
+
+template <int NTW, int D, int R>
+hipError_t stream_rows(const FfnRows& ffn, const uint8_t* wq, const uint8_t* s_u8,
+                       const uint8_t* a_u8, const float* sw, void* Y, int out_type, int N, int K,
+                       int group, int ks, hipStream_t st) {
+    const dim3 grid(N / (kTileN * NTW)), block(64 * ks);
+    const size_t pbytes = (size_t)2 * stream_param_span<NTW>() * (K / group) * 64;
+    const size_t xbytes = (size_t)ks * 2048;  // X slots
+    const size_t rbytes = (size_t)ks * NTW * 256 * sizeof(int);
+    const bool ldsp = pbytes + xbytes <= 128 * 1024;
+    const size_t used = (ldsp ? pbytes : 0) + xbytes;
+    const size_t lds = used > rbytes ? used : rbytes;
+#define ROWS(O, G, P)                                                                        \
+    hipLaunchKernelGGL((w4a8_stream_rows_kernel<NTW, D, O, G, P, R>), grid, block, lds, st, \
+                       ffn, wq, s_u8, a_u8, sw, Y, N, K, ks)
+#define ROWS_GROUP(O, P)                \
+    do {                                \
+        if (group == 64) ROWS(O, 64, P); \
+        else ROWS(O, 128, P);           \
+    } while (0)
+    if (ldsp) {
+        if (out_type == 2) ROWS_GROUP(2, true);
+        else ROWS_GROUP(0, true);
+    } else {
+        if (out_type == 2) ROWS_GROUP(2, false);
+        else ROWS_GROUP(0, false);
+    }
+#undef ROWS_GROUP
+#undef ROWS
+    return hipGetLastError();
+}
 
 template <int NTW, int D, int RB>
 hipError_t stream_glu(const int8_t* X, const float* sx, const uint8_t* wq, const uint8_t* s_u8,
-                      const uint8_t* a_u8, const float* sw, int act, const FfnOut& ffn, int M,
+                      const uint8_t* a_u8, const float* sw, int act, const FfnRows& ffn, int M,
                       int F, int K, int group, int ks, hipStream_t st) {
     const dim3 grid(F / (kTileN * NTW / 2), (M + 16 * RB - 1) / (16 * RB)), block(64 * ks);
     const size_t pbytes = (size_t)4 * stream_param_span<NTW / 2>() * (K / group) * 64;
@@ -50,11 +92,27 @@ hipError_t stream_glu(const int8_t* X, const float* sx, const uint8_t* wq, const
 
 }  // namespace
 
+hipError_t launch_w4a8_stream_rows(const float* h, const unsigned* tops, int ntops,
+                                   const uint8_t* wq, const uint8_t* s_u8, const uint8_t* a_u8,
+                                   const float* sw, void* Y, int out_type, int M, int N, int K,
+                                   int group, StreamCfg cfg, hipStream_t st) {
+    const FfnRows ffn{const_cast<float*>(h), const_cast<unsigned*>(tops), ntops};
+#define ROWS_NTW(W, D, R) \
+    return stream_rows<W, D, R>(ffn, wq, s_u8, a_u8, sw, Y, out_type, N, K, group, cfg.ks, st)
+    if (cfg.nt_per_wave == 2) {
+        if (M == 1) ROWS_NTW(2, 2, 1);
+        ROWS_NTW(2, 2, 2);
+    }
+    if (M == 1) ROWS_NTW(1, 3, 1);
+    ROWS_NTW(1, 3, 2);
+#undef ROWS_NTW
+}
+
 hipError_t launch_w4a8_stream_glu(const int8_t* X, const float* sx, const uint8_t* wq,
                                   const uint8_t* s_u8, const uint8_t* a_u8, const float* sw,
                                   int act, float* h, unsigned* tops, int M, int F, int K,
                                   int group, StreamCfg cfg, hipStream_t st) {
-    const FfnOut ffn{h, tops};
+    const FfnRows ffn{h, tops, F / 16};
 #define GLU_NTW(W, D, R)                                                                       \
     return stream_glu<W, D, R>(X, sx, wq, s_u8, a_u8, sw, act, ffn, M, F, K, group, cfg.ks, st)
     switch (cfg.nt_per_wave * 8 + cfg.rb) {

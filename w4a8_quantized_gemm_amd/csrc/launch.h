@@ -186,6 +186,13 @@ hipError_t launch_w4a8_stream_glu(const int8_t* X, const float* sx, const uint8_
                                   const uint8_t* s_u8, const uint8_t* a_u8, const float* sw,
                                   int act, float* h, unsigned* tops, int M, int F, int K,
                                   int group, StreamCfg cfg, hipStream_t st);
+// The down product of one or two (kFewRows) float32 rows, which its workgroups
+// quantise (one or two tiles per workgroup).
+constexpr int kFewRows = 2;
+hipError_t launch_w4a8_stream_rows(const float* h, const unsigned* tops, int ntops,
+                                   const uint8_t* wq, const uint8_t* s_u8, const uint8_t* a_u8,
+                                   const float* sw, void* Y, int out_type, int M, int N, int K,
+                                   int group, StreamCfg cfg, hipStream_t st);
 // INT8 of h rows whose maxima are those of `ntops` values a row.
 hipError_t launch_ffn_quant(const float* h, const unsigned* tops, int ntops, int M, int F,
                             int8_t* hq, float* sh, hipStream_t st);

@@ -418,7 +418,7 @@ __device__ __forceinline__ void mfma16_lora_epilogue(v4i (&acc)[MT / 16][4], uin
 // in a loop, as with adapters.
 template <int NB, int GLU, typename Read>
 __device__ __forceinline__ void mfma16_glu_epilogue(Read read, const float* sxs, const float* sw,
-                                                    const FfnOut& out, int m0, int r0, int c0,
+                                                    const FfnRows& out, int m0, int r0, int c0,
                                                     int row_hi, int F) {
     constexpr int PB = 2;
     const int lane = threadIdx.x & 63;
@@ -474,7 +474,7 @@ __device__ __forceinline__ void mfma16_body(
     const uint8_t* __restrict__ s_u8, const uint8_t* __restrict__ a_u8,
     const float* __restrict__ sw, void* __restrict__ Y, int* __restrict__ part, int M, int N,
     int K, int tiles_n, int tiles_m, int splits, const int* __restrict__ offsets,
-    const LoraArgs& lora, const FfnOut& ffn = {}) {
+    const LoraArgs& lora, const FfnRows& ffn = {}) {
     static_assert(GLU == 0 || (!PARTIAL && !W8 && LORA == 0), "plain tiles");
     static_assert(LORA == 0 || (OUT == 0 && !PARTIAL && !W8 && KIN == 1), "one rounding to fp16");
     static_assert(KIN == 1 || (KIN == 2 && MT <= 128), "K parts: up to 128-row tiles");

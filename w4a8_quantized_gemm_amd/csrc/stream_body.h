@@ -18,6 +18,11 @@ __host__ __device__ constexpr int stream_param_span() {
     return (NTW + 3) / 4 + 1;
 }
 
+__device__ __forceinline__ v4i buf_load_v4(__amdgpu_buffer_rsrc_t r, unsigned voff,
+                                           unsigned soff) {
+    return __builtin_bit_cast(v4i, __builtin_amdgcn_raw_buffer_load_b128(r, voff, soff, 0));
+}
+
 // Swizzled 16-byte piece position of row R's piece c in a 16 x 128-byte X
 // tile held in LDS (row stride 128 bytes): conflict-free for the row-wise
 // writes and for the MFMA-layout reads below.
@@ -56,17 +61,22 @@ constexpr int kWkLQQ = 0, kWkW8 = 1, kWkF8 = 2, kWkF8G = 3;
 
 // LORA (1: fp16, 2: bfloat16 adapters; W4A8 to fp16 only): the epilogue adds
 // each row's low-rank adapter to its scaled sums before the one rounding.
+// HROWS (1 or 2; W4A8, one row block): X is not INT8 but the float32 rows `ffn` of
+// that many rows with their partial maxima, and a wave quantises each K-tile as
+// it comes to it (the rows' scales are taken once, behind the first loads).
 // GLU (1: SiLU, 2: GELU; W4A8 only): the first half of a workgroup's tiles lie
 // in the gate half of N = 2F, the others are the same ones of the up half, and
 // the epilogue writes act(gate) up with the largest of each row's 16 channels.
-template <int NTW, int D, int OUT, int GROUP, bool LDSP, int WK, int RB, int LORA, int GLU = 0>
+template <int NTW, int D, int OUT, int GROUP, bool LDSP, int WK, int RB, int LORA, int GLU = 0,
+          int HROWS = 0>
 __device__ __forceinline__ void stream_body(
     const int8_t* __restrict__ X, const float* __restrict__ sx, const uint8_t* __restrict__ wq,
     const uint8_t* __restrict__ s_u8, const uint8_t* __restrict__ a_u8,
     const float* __restrict__ sw, void* __restrict__ Y, int M, int N, int K, int ks,
     const int* __restrict__ offsets, const float* __restrict__ fsc,
-    const float* __restrict__ tsc, const LoraArgs& lora, const FfnOut& ffn = {}) {
+    const float* __restrict__ tsc, const LoraArgs& lora, const FfnRows& ffn = {}) {
     static_assert(GLU == 0 || (LORA == 0 && WK == kWkLQQ && NTW % 2 == 0), "pairs of tiles");
+    static_assert(HROWS == 0 || (HROWS <= 2 && LORA == 0 && GLU == 0 && WK == kWkLQQ && RB == 1), "few float rows");
     static_assert(LORA == 0 || (OUT == 0 && WK == kWkLQQ), "adapters: W4A8 to fp16");
     constexpr bool W8 = WK == kWkW8;
     constexpr bool F8 = WK == kWkF8 || WK == kWkF8G;
@@ -114,7 +124,9 @@ __device__ __forceinline__ void stream_body(
     auto kt_of = [&](int i) { return wave + ks * i; };
 
     const __amdgpu_buffer_rsrc_t x_rsrc =
-        __builtin_amdgcn_make_buffer_rsrc(const_cast<int8_t*>(X), (short)0, M * K, 0x00020000);
+        HROWS ? __builtin_amdgcn_make_buffer_rsrc(ffn.h, (short)0, 4 * M * K, 0x00020000)
+              : __builtin_amdgcn_make_buffer_rsrc(const_cast<int8_t*>(X), (short)0, M * K,
+                                                  0x00020000);
     const __amdgpu_buffer_rsrc_t w_rsrc = __builtin_amdgcn_make_buffer_rsrc(
         const_cast<uint8_t*>(wq), (short)0, (int)((size_t)N * K / (W8 ? 1 : 2)), 0x00020000);
     const __amdgpu_buffer_rsrc_t f_rsrc = __builtin_amdgcn_make_buffer_rsrc(
@@ -128,8 +140,12 @@ __device__ __forceinline__ void stream_body(
     // the LDS re-layout, lane l takes 16-byte piece (l & 7) of rows
     // m0 + (l >> 3) and m0 + 8 + (l >> 3); otherwise lane (r, G) loads its
     // MFMA operand directly: row m0 + r, columns 32G .. 32G+31.
+    // (HROWS: 64 / HROWS lanes take 2 HROWS consecutive elements each of a row)
+    constexpr int HL = HROWS ? 64 / HROWS : 64;  // lanes of a row
+    const int hrow = lane / HL, hcol = 2 * HROWS * (lane % HL);
     const unsigned xvoff =
-        kXlds ? (unsigned)(m0 + (lane >> 3)) * (unsigned)K + 16u * (unsigned)(lane & 7)
+        HROWS ? 4u * ((unsigned)hrow * (unsigned)K + (unsigned)hcol)
+        : kXlds ? (unsigned)(m0 + (lane >> 3)) * (unsigned)K + 16u * (unsigned)(lane & 7)
               : (unsigned)(m0 + r) * (unsigned)K + 32u * (unsigned)G;
     const unsigned xvoff8 = kXlds ? xvoff + 8u * (unsigned)K : xvoff + 16u;
     const unsigned wvoff = (unsigned)lane * 16u;
@@ -157,9 +173,15 @@ __device__ __forceinline__ void stream_body(
         float f[NF];
     };
     auto issue = [&](int kt, Stage& st) {
-        const unsigned so = (unsigned)(kt * kTileK);
+        const unsigned so = (unsigned)(kt * kTileK * (HROWS ? 4 : 1));
+        if constexpr (HROWS == 1) {
+            const auto v = __builtin_amdgcn_raw_buffer_load_b64(x_rsrc, xvoff, so, 0);
+            st.x0[0] = v4i{(int)v[0], (int)v[1], 0, 0};
+        } else if constexpr (HROWS == 2) {
+            st.x0[0] = buf_load_v4(x_rsrc, xvoff, so);
+        }
 #pragma unroll
-        for (int rb = 0; rb < RB; ++rb) {
+        for (int rb = 0; rb < (HROWS ? 0 : RB); ++rb) {
             const unsigned ro = 16u * (unsigned)rb * (unsigned)K;  // row block rb
             st.x0[rb] = __builtin_bit_cast(
                 v4i, __builtin_amdgcn_raw_buffer_load_b128(x_rsrc, xvoff + ro, so, 0));
@@ -214,6 +236,8 @@ __device__ __forceinline__ void stream_body(
 #pragma unroll
         for (int t = 0; t < NTW; ++t) acc[rb][t] = Acc{};
 
+    [[maybe_unused]] __shared__ unsigned htops[HROWS ? HROWS * 16 : 1];
+    [[maybe_unused]] float hscale = 1.0f, hinv = 1.0f;  // of the lane's row
     // Multiply-accumulate of the K-tile held in stage S.
     auto consume = [&](const Stage& S, int kt) {
         v4i x0[RB], x1[RB];
@@ -221,7 +245,22 @@ __device__ __forceinline__ void stream_body(
         for (int rb = 0; rb < RB; ++rb) {
             x0[rb] = S.x0[rb];
             x1[rb] = S.x1[rb];
-            if constexpr (kXlds) {
+            if constexpr (HROWS) {
+                // the lane's codes; the other rows stay the zeros that were put
+                // there at the start
+                float v[4] = {};
+#pragma unroll
+                for (int j = 0; j < 2 * HROWS; ++j) {
+                    const int b = S.x0[0][j];
+                    v[j] = __builtin_bit_cast(float, b);
+                }
+                const unsigned q = quant4_fast(v[0], v[1], v[2], v[3], hscale, hinv);
+                uint8_t* at = xslot + xpiece(hrow, hcol >> 4) + (hcol & 15);
+                if constexpr (HROWS == 1) *reinterpret_cast<unsigned short*>(at) = (unsigned short)q;
+                else *reinterpret_cast<unsigned*>(at) = q;
+                x0[0] = *reinterpret_cast<const v4i*>(xslot + xr0);
+                x1[0] = *reinterpret_cast<const v4i*>(xslot + xr1);
+            } else if constexpr (kXlds) {
                 // X tile -> MFMA layout through this wave's LDS slot (LDS
                 // operations of one wave complete in order).
                 uint8_t* xs = xslot + rb * 2048;
@@ -305,7 +344,27 @@ __device__ __forceinline__ void stream_body(
                 *reinterpret_cast<v4i*>(lds_a + to + q * 16) = va;
             }
         }
+        if constexpr (!HROWS) __syncthreads();
+    }
+    if constexpr (HROWS) {
+        // largest of each row's parts: every wave takes a share of all rows
+        unsigned top[HROWS] = {};
+        for (int q = tid; q < ffn.ntops; q += blockDim.x)
+#pragma unroll
+            for (int m = 0; m < HROWS; ++m)
+                top[m] = MaxU32{}(top[m], ffn.tops[(size_t)m * ffn.ntops + q]);
+#pragma unroll
+        for (int m = 0; m < HROWS; ++m) {
+            top[m] = wave_reduce(top[m], MaxU32{});
+            if (lane == 0) htops[m * 16 + wave] = top[m];
+        }
+        *reinterpret_cast<v4i*>(xslot + 32 * lane) = v4i{0, 0, 0, 0};
+        *reinterpret_cast<v4i*>(xslot + 32 * lane + 16) = v4i{0, 0, 0, 0};
         __syncthreads();
+        unsigned all = 0;
+        for (int w = 0; w < ks; ++w) all = MaxU32{}(all, htops[hrow * 16 + w]);
+        hscale = row_scale_bits(all);
+        hinv = __fdiv_rn(1.0f, hscale);
     }
 
     int i = 0;
@@ -428,7 +487,15 @@ __device__ __forceinline__ void stream_body(
             } else if (OUT == 1) {
                 reinterpret_cast<int*>(Y)[(size_t)m * N + n] = sum;
             } else {
-                const float y = ((float)sum * sx[m]) * sw[n];
+                float xs;
+                if constexpr (HROWS) {
+                    unsigned all = 0;
+                    for (int w = 0; w < ks; ++w) all = MaxU32{}(all, htops[m * 16 + w]);
+                    xs = row_scale_bits(all);
+                } else {
+                    xs = sx[m];
+                }
+                const float y = ((float)sum * xs) * sw[n];
                 reinterpret_cast<unsigned short*>(Y)[(size_t)m * N + n] = f32_to_out16_bits<OUT>(y);
             }
         }
