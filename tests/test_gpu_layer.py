@@ -136,6 +136,21 @@ NORM = [  # M, K, x, y, post, gate, bias, layer, out
     (512, 2080, "bf16", "f16", True, "ids", True, False, "int8"),
     (600, 512, "f16", "f32", False, "row", False, True, "e4m3"),
     (700, 4096, "bf16", "f16", False, "none", False, False, "int8"),
+    # both sides of every row width's limit
+    (259, 16, "bf16", "f16", True, "row", True, True, "int8"),
+    (257, 1024, "f16", "bf16", True, "ids", True, True, "int8"),
+    (258, 1040, "bf16", "f16", True, "row", False, False, "e4m3"),
+    (260, 2048, "f32", "f16", True, "none", True, True, "int8"),
+    (261, 2064, "bf16", None, False, "none", False, False, "int8"),
+    (300, 4112, "bf16", "f16", True, "row", True, True, "bf16"),
+    (257, 6144, "f16", "f32", True, "all", True, False, "int8"),
+    (257, 6160, "bf16", "f16", True, "row", False, True, "e4m3"),
+    (256, 8192, "bf16", "f16", True, "row", True, True, "int8"),
+    (257, 8208, "f32", "f32", True, "row", True, True, "int8"),
+    (258, 12288, "bf16", "f16", True, "row", False, False, "int8"),
+    (257, 12304, "f16", "f16", True, "ids", True, True, "f16"),
+    (257, 32768, "f32", "f32", True, "row", True, True, "e4m3"),
+    (257, 32784, "bf16", "f16", False, "none", False, False, "int8"),
     (513, 5136, "f32", "bf16", True, "all", True, True, "f16"),
     (520, 8192, "f16", "f16", True, "row", False, False, "int8"),
     (515, 16384, "bf16", "bf16", False, "ids", True, True, "bf16"),

@@ -24,6 +24,11 @@ namespace w4a8 {
 
 namespace {
 
+// pairs, for the conversions that round two floats at once (nearest even)
+typedef float v2f __attribute__((ext_vector_type(2)));
+typedef _Float16 v2h __attribute__((ext_vector_type(2)));
+typedef __bf16 v2b __attribute__((ext_vector_type(2)));
+
 template <int CTRL>
 __device__ __forceinline__ double dpp_step(double v) {
     const uint2 u = __builtin_bit_cast(uint2, v);
@@ -94,17 +99,17 @@ __device__ __forceinline__ void store_row8(void* X, int type, size_t m, int K, i
         p[1] = v4f{v[4], v[5], v[6], v[7]};
         return;
     }
-    unsigned w[4];
+    v4i w;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-        const unsigned short a =
-            type == 1 ? f32_to_f16_bits(v[2 * j]) : f32_to_bf16_bits(v[2 * j]);
-        const unsigned short b =
-            type == 1 ? f32_to_f16_bits(v[2 * j + 1]) : f32_to_bf16_bits(v[2 * j + 1]);
-        w[j] = a | ((unsigned)b << 16);
+        float a = v[2 * j], b = v[2 * j + 1];
+        asm("" : "+v"(a), "+v"(b));  // rounded to float32 before they are converted
+        if (type == 1)
+            w[j] = __builtin_bit_cast(int, __builtin_convertvector((v2f{a, b}), v2h));
+        else
+            w[j] = __builtin_bit_cast(int, __builtin_convertvector((v2f{a, b}), v2b));
     }
-    reinterpret_cast<v4i*>(reinterpret_cast<unsigned short*>(X) + m * K)[i] =
-        v4i{(int)w[0], (int)w[1], (int)w[2], (int)w[3]};
+    reinterpret_cast<v4i*>(reinterpret_cast<unsigned short*>(X) + m * K)[i] = w;
 }
 
 // Gate row of row m: its own, the batch's, or the one it names (-1: none).
@@ -142,17 +147,19 @@ __device__ __forceinline__ uint2 e4m3_codes(const float (&n)[8], float s) {
 }  // namespace
 
 // XT, YT: element types of the residual stream and of the block's output
-// (YT = -1: no block).  A row of at most 8 TPB CH elements.
+// (YT = -1: no block).  A row of at most 8 TPB CH elements by TPB threads; rows
+// of one wave (TPB = 64) lie four to a workgroup and meet no barrier.
 template <int XT, int YT, int CH, int TPB>
-__global__ __launch_bounds__(TPB) void norm_kernel(NormArgs a) {
+__global__ __launch_bounds__(TPB == 64 ? 256 : TPB) void norm_kernel(NormArgs a) {
     constexpr bool HASY = YT >= 0;
     constexpr int YL = HASY ? YT : 0;
     constexpr int W = TPB / 64;
     __shared__ double sums[4][W];
     __shared__ unsigned maxs[W];
     const int K = a.K, n8 = K / 8;
-    const size_t m = blockIdx.x;
-    const int tid = threadIdx.x;
+    const size_t m = TPB == 64 ? blockIdx.x * 4 + (threadIdx.x >> 6) : blockIdx.x;
+    const int tid = TPB == 64 ? threadIdx.x & 63 : threadIdx.x;
+    if (TPB == 64 && (int)m >= a.M) return;
 
     Raw8<XT> xr[CH];
     Raw8<YL> yr[HASY ? CH : 1], gr[HASY ? CH : 1];
@@ -391,22 +398,37 @@ __global__ __launch_bounds__(1024) void norm_long_kernel(NormArgs a) {
 
 namespace {
 
+// Threads and chunks of eight elements a thread for a row.  At most a row per
+// CU: as many threads as the row feeds, for the shortest chain.  More rows: two
+// chunks a thread hide the reductions behind the other rows' loads with the
+// fewest idle threads.  us, threads x chunks (16-bit x and y to INT8, residual
+// sum and norm):
+//   8192 x 8192: 512 x 2 84, 256 x 4 89, 1024 x 1 112     8192 x 1024: 64 x 2 15.6,
+//   8192 x 4096: 256 x 2 44.4, 512 x 1 50.4                 256 x 1 20.1
+//   8192 x 2048: 128 x 2 25.5, 256 x 1 28.0, 64 x 4 28.2  2048 x 16384: 512 x 4 51.1,
+//   1000 x 5120 (gated, two norms): 256 x 3 13.9, 512 x 2 14.9   1024 x 2 54.5
 template <int XT, int YT>
 void launch_norm_types(const NormArgs& a, hipStream_t st) {
     const int n8 = a.K / 8;
-#define NORM(CH, TPB)                                                                       \
-    if (n8 <= TPB * CH) {                                                                   \
-        hipLaunchKernelGGL((norm_kernel<XT, YT, CH, TPB>), dim3(a.M), dim3(TPB), 0, st, a); \
-        return;                                                                             \
+#define NORM(CH, TPB)                                                                    \
+    if (n8 <= TPB * CH) {                                                                \
+        const int rows = TPB == 64 ? 4 : 1;                                              \
+        hipLaunchKernelGGL((norm_kernel<XT, YT, CH, TPB>), dim3((a.M + rows - 1) / rows), \
+                           dim3(rows * TPB), 0, st, a);                                  \
+        return;                                                                          \
     }
-    NORM(1, 256)
-    if (a.M < 512) {
+    if (a.M <= 256) {
+        NORM(1, 256)
         NORM(1, 1024)
         NORM(2, 1024)
     } else {
+        NORM(2, 64)
+        NORM(2, 128)
         NORM(2, 256)
-        NORM(4, 256)
-        NORM(8, 256)
+        NORM(3, 256)
+        NORM(2, 512)
+        NORM(3, 512)
+        NORM(4, 512)
     }
     NORM(4, 1024)
 #undef NORM
