@@ -398,14 +398,14 @@ __global__ __launch_bounds__(1024) void norm_long_kernel(NormArgs a) {
 
 namespace {
 
-// Threads and chunks of eight elements a thread for a row.  At most a row per
-// CU: as many threads as the row feeds, for the shortest chain.  More rows: two
-// chunks a thread hide the reductions behind the other rows' loads with the
-// fewest idle threads.  us, threads x chunks (16-bit x and y to INT8, residual
-// sum and norm):
-//   8192 x 8192: 512 x 2 84, 256 x 4 89, 1024 x 1 112     8192 x 1024: 64 x 2 15.6,
-//   8192 x 4096: 256 x 2 44.4, 512 x 1 50.4                 256 x 1 20.1
-//   8192 x 2048: 128 x 2 25.5, 256 x 1 28.0, 64 x 4 28.2  2048 x 16384: 512 x 4 51.1,
+// Threads and chunks of eight elements a thread for a row: two chunks a thread
+// where that is possible, fewer threads only where many rows share the CUs.  us,
+// threads x chunks (16-bit x and y to INT8, residual sum and norm):
+//   16 x 8192: 512 x 2 4.4, 1024 x 1 5.5, 256 x 4 5.4     8192 x 1024: 64 x 2 15.6,
+//   1 x 4096: 256 x 2 3.1, 1024 x 1 3.3, 64 x 8 6.4         256 x 1 20.1
+//   16 x 2048: 256 x 2 3.6, 128 x 2 3.9, 1024 x 1 3.8     8192 x 2048: 128 x 2 25.5,
+//   8192 x 8192: 512 x 2 84, 256 x 4 89, 1024 x 1 112       256 x 1 28.0, 64 x 4 28.2
+//   8192 x 4096: 256 x 2 44.4, 512 x 1 50.4               2048 x 16384: 512 x 4 51.1,
 //   1000 x 5120 (gated, two norms): 256 x 3 13.9, 512 x 2 14.9   1024 x 2 54.5
 template <int XT, int YT>
 void launch_norm_types(const NormArgs& a, hipStream_t st) {
@@ -417,19 +417,15 @@ void launch_norm_types(const NormArgs& a, hipStream_t st) {
                            dim3(rows * TPB), 0, st, a);                                  \
         return;                                                                          \
     }
-    if (a.M <= 256) {
-        NORM(1, 256)
-        NORM(1, 1024)
-        NORM(2, 1024)
-    } else {
+    if (a.M > 256) {
         NORM(2, 64)
         NORM(2, 128)
-        NORM(2, 256)
-        NORM(3, 256)
-        NORM(2, 512)
-        NORM(3, 512)
-        NORM(4, 512)
     }
+    NORM(2, 256)
+    if (a.M > 256) NORM(3, 256)
+    NORM(2, 512)
+    NORM(3, 512)
+    NORM(4, 512)
     NORM(4, 1024)
 #undef NORM
     hipLaunchKernelGGL((norm_long_kernel<XT, YT>), dim3(a.M), dim3(1024), 0, st, a);
