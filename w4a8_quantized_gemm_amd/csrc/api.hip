@@ -716,6 +716,7 @@ W4A8_EXPORT w4a8_status_t w4a8_norm_quant(
     a.x_scale = x_scale;
     a.y_scale = y_scale;
     a.eps = eps;
+    a.inv_k = 1.0 / K;
     return hip_status(w4a8::launch_norm_quant(a, x_type, y_type, stream));
 }
 

@@ -172,6 +172,7 @@ struct NormArgs {
     float* sx;
     int gate_rows, layer, out_type, M, K;  // out_type: W4A8_IN_*, 3 INT8, 4 e4m3
     float x_scale, y_scale, eps;
+    double inv_k;  // 1 / K
 };
 hipError_t launch_norm_quant(const NormArgs& a, int x_type, int y_type, hipStream_t st);
 

@@ -122,8 +122,19 @@ __device__ __forceinline__ int gate_row(const NormArgs& a, int m) {
     return a.gate_rows == 1 ? 0 : m;
 }
 
-__device__ __forceinline__ float inverse_rms(double sum, int K, float eps) {
-    return (float)(1.0 / sqrt(sum / (double)K + (double)eps));
+// float32(1 / sqrt(sum / K + eps)): the hardware's estimate and two Newton steps,
+// which leave about 2^-52 (a correctly rounded square root and quotient in
+// float64 are six times the instructions, in every wave of a row).  A row whose
+// squares add up to infinity gets 0.
+__device__ __forceinline__ float inverse_rms(double sum, double inv_k, float eps) {
+    const double v = __builtin_fma(sum, inv_k, (double)eps);
+    double y = __builtin_amdgcn_rsq(v);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const double e = __builtin_fma(-v * y, y, 1.0);
+        y = __builtin_fma(0.5 * y, e, y);
+    }
+    return v == __builtin_inf() ? 0.0f : (float)y;
 }
 
 // Codes of eight elements (finite) with scale s.
@@ -188,39 +199,38 @@ __global__ __launch_bounds__(TPB == 64 ? 256 : TPB) void norm_kernel(NormArgs a)
         }
     }
 
-    // r (and mean) of v, whose elements past the row end are zero
-    auto statistics = [&](const float (&v)[CH][8], float& mean, int at) {
-        mean = 0.0f;
+    // v = norm(v); elements past the row end stay zero
+    auto normed = [&](float (&v)[CH][8], const float* w, const float* bias, int at) {
+        double s = 0.0;
         if (a.layer) {
-            double s = 0.0;
 #pragma unroll
             for (int j = 0; j < CH; ++j)
 #pragma unroll
                 for (int e = 0; e < 8; ++e) s += (double)v[j][e];
-            mean = (float)(block_sum64<TPB>(s, sums[at]) / (double)K);
-        }
-        double s = 0.0;
+            const float mean = (float)(block_sum64<TPB>(s, sums[at]) * a.inv_k);
+            s = 0.0;
 #pragma unroll
-        for (int j = 0; j < CH; ++j) {
-            if (tid + TPB * j >= n8) continue;
+            for (int j = 0; j < CH; ++j) {
+                if (tid + TPB * j >= n8) continue;
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const double d = (double)(v[j][e] - mean);
-                s = __builtin_fma(d, d, s);
+                for (int e = 0; e < 8; ++e) v[j][e] = v[j][e] - mean;
             }
         }
-        return inverse_rms(block_sum64<TPB>(s, sums[at + 1]), K, a.eps);
-    };
-    auto normed = [&](float (&v)[CH][8], const float* w, const float* bias, int at) {
-        float mean;
-        const float r = statistics(v, mean, at);
+#pragma unroll
+        for (int j = 0; j < CH; ++j)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const double d = (double)v[j][e];
+                s = __builtin_fma(d, d, s);
+            }
+        const float r = inverse_rms(block_sum64<TPB>(s, sums[at + 1]), a.inv_k, a.eps);
 #pragma unroll
         for (int j = 0; j < CH; ++j) {
             const int i = tid + TPB * j;
             if (i >= n8) continue;
             const F8v wv = load_f8(w, i);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) v[j][e] = ((v[j][e] - mean) * r) * wv.v[e];
+            for (int e = 0; e < 8; ++e) v[j][e] = (v[j][e] * r) * wv.v[e];
             if (bias) {
                 const F8v bv = load_f8(bias, i);
 #pragma unroll
@@ -228,6 +238,7 @@ __global__ __launch_bounds__(TPB == 64 ? 256 : TPB) void norm_kernel(NormArgs a)
             }
         }
     };
+    const bool scaled = a.x_scale != 1.0f || a.y_scale != 1.0f;
 
     float v[CH][8];
     if constexpr (HASY) {
@@ -250,8 +261,13 @@ __global__ __launch_bounds__(TPB == 64 ? 256 : TPB) void norm_kernel(NormArgs a)
         for (int j = 0; j < CH; ++j) {
             const int i = tid + TPB * j;
             const Row8<XT> x = widen8<XT>(xr[j]);
+            if (scaled) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) v[j][e] = x.v[e] * a.x_scale + v[j][e] * a.y_scale;
+                for (int e = 0; e < 8; ++e) v[j][e] = x.v[e] * a.x_scale + v[j][e] * a.y_scale;
+            } else {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) v[j][e] = x.v[e] + v[j][e];
+            }
             if (i < n8) store_row8(a.xout, XT, m, K, i, v[j]);
         }
     } else {
@@ -350,7 +366,7 @@ __global__ __launch_bounds__(1024) void norm_long_kernel(NormArgs a) {
 #pragma unroll
                 for (int e = 0; e < 8; ++e) s += (double)v[e];
             }
-            mu = (float)(block_sum64<TPB>(s, sums[at]) / (double)K);
+            mu = (float)(block_sum64<TPB>(s, sums[at]) * a.inv_k);
         }
         double s = 0.0;
         for (int i = tid; i < n8; i += TPB) {
@@ -362,7 +378,7 @@ __global__ __launch_bounds__(1024) void norm_long_kernel(NormArgs a) {
                 s = __builtin_fma(d, d, s);
             }
         }
-        inv = inverse_rms(block_sum64<TPB>(s, sums[at + 1]), K, a.eps);
+        inv = inverse_rms(block_sum64<TPB>(s, sums[at + 1]), a.inv_k, a.eps);
     };
     if constexpr (HASY)
         if (a.y_weight) statistics(block_out, y_mean, y_r, 0);
