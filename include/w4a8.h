@@ -519,9 +519,10 @@ enum {
  *     selects no gate: that row's factor is 1), else m, or 0 if gate_rows is 1.
  *   A row whose n is not finite throughout gets sx = NaN and codes 0: the
  *     GEMMs return NaN for it, and no other row is affected.
- * K % 16 == 0; eps > 0; eps, x_scale and y_scale finite (W4A8_ERR_UNSUPPORTED
- * otherwise); gate_rows is 1 or M without gate_ids.  W4A8_ERR_NULL_PTR also for
- * a bias without its weight, and for y_weight or gate without Y.  X, Y, gate, Xout, out 16-byte
+ * K % 16 == 0, M < 2^22; gate_rows is 1 or M without gate_ids; eps > 0, and
+ * eps, x_scale and y_scale finite (W4A8_ERR_UNSUPPORTED otherwise).
+ * W4A8_ERR_NULL_PTR also for a bias without its weight, for y_weight or gate
+ * without Y, and for gate_ids without gate.  X, Y, gate, Xout and out 16-byte
  * aligned, the others 4-byte.
  */
 w4a8_status_t w4a8_norm_quant(const void* X, int x_type, const void* Y,

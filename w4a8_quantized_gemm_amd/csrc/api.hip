@@ -680,7 +680,8 @@ W4A8_EXPORT w4a8_status_t w4a8_norm_quant(
         return W4A8_ERR_UNSUPPORTED;
     if (!(eps > 0.0f) || !std::isfinite(eps) || !std::isfinite(x_scale) || !std::isfinite(y_scale))
         return W4A8_ERR_UNSUPPORTED;
-    if (M < 0 || K <= 0 || K % 16 != 0) return W4A8_ERR_SHAPE;
+    // (a workgroup per row: at most 2^32 threads in a launch)
+    if (M < 0 || M >= (1 << 22) || K <= 0 || K % 16 != 0) return W4A8_ERR_SHAPE;
     if (gate && (gate_rows < 1 || (!gate_ids && gate_rows != 1 && gate_rows != M)) && M > 0)
         return W4A8_ERR_SHAPE;
     if (M == 0) return W4A8_OK;  // nothing to read or write
@@ -747,16 +748,18 @@ struct FfnPlan {
         up_stream = M <= 32 || t64 < 128;
         if (up_stream) {
             // Row blocks: two from 17 rows on.  Four tiles (two of each half)
-            // where that leaves workgroups enough, else two: one block, B 42.2 /
-            // 44.0 at 16 rows and 41.9 / 40.6 at one, A 14.5 / 12.6; two blocks, B
-            // 46.3 / 48.0 at 17 rows, C 15.3 / 17.3 at 47, A 16.2 / 14.1 at 17.
+            // where that leaves workgroups enough, else two: one block, B 41.7 /
+            // 43.6 at 16 rows and 40.0 / 38.7 at one, A 13.7 / 12.8; two blocks, B
+            // 44.8 / 48.9 at 17 rows, C 15.2 / 16.5 at 47, A 16.1 / 14.5 at 17.
             up.rb = M <= 16 ? 1 : 2;
             const long long wide = (long long)(F / 32) * ((M + 16 * up.rb - 1) / (16 * up.rb));
             up.nt_per_wave = M > 1 && wide >= (up.rb == 1 ? 768 : 400) ? 4 : 2;
-            // Waves splitting K: four; eight for few workgroups (D, 17 rows: 5.7 /
-            // 6.5), two for very many (D, 300 rows: 10.1 / 12.3).
+            // Waves splitting K: eight with one row block (eight / four: B, one row,
+            // 38.7 / 39.7; A, 11.7 / 12.2); with two, four (A, 17 rows: 15.2 / 14.5),
+            // eight for few workgroups (D, 17 rows: 5.7 / 6.5), two for very many (D,
+            // 300 rows: four 12.3, two 10.1).
             const long long wgs = up.nt_per_wave == 4 ? wide : 2 * wide;
-            up.ks = wgs <= 352 ? 8 : (M > 64 && wgs > 640) ? 2 : 4;
+            up.ks = up.rb == 1 || wgs <= 352 ? 8 : (M > 64 && wgs > 640) ? 2 : 4;
             while (up.ks > 1 && k_tiles(H) < up.ks) up.ks /= 2;
             return;
         }
