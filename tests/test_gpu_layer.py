@@ -374,6 +374,19 @@ FFN = [
     (513, 4096, 384, 128, "gelu", "bf16"),
     (1000, 512, 5504, 64, "silu", "f16"),
     (2050, 256, 4224, 128, "silu", "bf16"),
+    # one case for each kernel that the plans choose: 64-row tiles of 64 channels
+    # of each half, of 128; 256-row tiles
+    (300, 256, 11008, 64, "gelu", "f16"),
+    (4296, 128, 8320, 128, "silu", "f16"),
+    # down: 64-row tiles with their K split, and where 256 does not divide H
+    (64, 8192, 6400, 128, "silu", "bf16"),
+    (50, 8192, 8320, 64, "silu", "f16"),
+    (3000, 384, 1408, 64, "gelu", "bf16"),
+    # down: the GEMM's own plans (two K parts, 32 x 32, 128- and 256-row tiles)
+    (300, 8192, 2048, 128, "silu", "bf16"),
+    (300, 8192, 16640, 128, "silu", "bf16"),
+    (2048, 8192, 128, 64, "gelu", "bf16"),
+    (2048, 8192, 8320, 128, "silu", "bf16"),
 ]
 
 
