@@ -135,18 +135,20 @@ def ffn(Xq, sx, W13, sw13, W2, sw2, act, dt):
     with np.errstate(invalid="ignore", over="ignore"):
         gu = acc * sx[:, None].astype(np.float64) * sw13.astype(np.float64)
         g, u = gu[:, :F], gu[:, F:]
+        # exp(-z) as a power of two: z's own error, and the rounded product
+        # z log2(e), which moves the power by |z| u
         if act == "gelu":
             z = GELU_C * g * (1.0 + 0.044715 * g * g)
             # z: g's three roundings counted up to three times (its cube), six
             # of its own operations and the two constants'
-            dz = np.abs(z) * (9 + 8) * U
+            dz = np.abs(z) * (9 + 8 + 1) * U
         else:
-            z, dz = g, np.abs(g) * 3 * U
+            z, dz = g, np.abs(g) * (3 + 1) * U
         h = g / (1.0 + np.exp(-z)) * u
-        # g and u three roundings each; exp(-z) moves by dz and its own 4 u
-        # (function and argument), of which the quotient feels at most all; sum,
-        # quotient and product u each
-        rel = 6 * U + dz + 4 * U + 3 * U
+        # g and u three roundings each; the power one unit in the last place
+        # (2 u) and dz, of which 1 / (1 + power) feels at most all; the sum u,
+        # the reciprocal one unit (2 u), the two products u each
+        rel = 6 * U + dz + 7 * U
     fin = np.isfinite(sx) & (np.abs(h) < 3.4e38).all(1)
     h = np.where(fin[:, None], h, 0.0)
     rel = np.where(fin[:, None], rel, 0.0)

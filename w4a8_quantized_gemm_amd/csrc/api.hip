@@ -741,8 +741,7 @@ struct FfnPlan {
 
     // Gate and up.  Streamed up to 32 rows, and while workgroups of 64 rows and
     // 64 channels of each half would leave half of the CUs without one (D, 133
-    // rows: 7.6 against 11 or more; C, 64 rows: 16 against 17.9, 96 rows: 21.4
-    // against 17.8).
+    // rows: 7.2 against 10.2; C, 64 rows: 16 against 18, 96 rows: 20.3 against 18.1).
     void plan_up(int M, int H, int F) {
         const long long t64 = (long long)(F / 64) * ((M + 63) / 64);
         up_stream = M <= 32 || t64 < 128;
@@ -750,16 +749,16 @@ struct FfnPlan {
             // Row blocks: two from 17 rows on.  Four tiles (two of each half)
             // where that leaves workgroups enough, else two: one block, B 41.7 /
             // 43.6 at 16 rows and 40.0 / 38.7 at one, A 13.7 / 12.8; two blocks, B
-            // 44.8 / 48.9 at 17 rows, C 15.2 / 16.5 at 47, A 16.1 / 14.5 at 17.
+            // 44.8 / 48.9 at 17 rows, C 15.5 / 16.4 at 47, A 16.1 / 14.5 at 17; D 11.2
+            // / 9.7 at 300.
             up.rb = M <= 16 ? 1 : 2;
             const long long wide = (long long)(F / 32) * ((M + 16 * up.rb - 1) / (16 * up.rb));
-            up.nt_per_wave = M > 1 && wide >= (up.rb == 1 ? 768 : 400) ? 4 : 2;
+            const bool four = up.rb == 1 ? M > 1 && wide >= 768 : M <= 64 && wide >= 400;
+            up.nt_per_wave = four ? 4 : 2;
             // Waves splitting K: eight with one row block (eight / four: B, one row,
             // 38.7 / 39.7; A, 11.7 / 12.2); with two, four (A, 17 rows: 15.2 / 14.5),
-            // eight for few workgroups (D, 17 rows: 5.7 / 6.5), two for very many (D,
-            // 300 rows: four 12.3, two 10.1).
-            const long long wgs = up.nt_per_wave == 4 ? wide : 2 * wide;
-            up.ks = up.rb == 1 || wgs <= 352 ? 8 : (M > 64 && wgs > 640) ? 2 : 4;
+            // and eight for few workgroups (D, 33 rows: 5.7 / 6.4).
+            up.ks = up.rb == 1 || (four ? wide : 2 * wide) <= 352 ? 8 : 4;
             while (up.ks > 1 && k_tiles(H) < up.ks) up.ks /= 2;
             return;
         }
