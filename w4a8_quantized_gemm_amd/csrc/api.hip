@@ -769,6 +769,10 @@ struct FfnPlan {
         // 64 rows (A, 300 rows: 45.9 against 53.8).
         const w4a8::MfmaPlan p = w4a8::plan_w4a8_mfma(M, 2 * F, H);
         up_mt = p.mt16 ? p.mt16 : p.mt;
+        // Short K: two 128-row workgroups per CU, one's epilogue beside the other's
+        // loop (8192 rows of A, whole block: 1046 against 1079; 4096 rows of B the
+        // other way, 2257 against 2216).
+        if (k_tiles(H) <= 32) up_mt = 128;
         const long long wgs = (long long)(F / 128) * ((M + up_mt - 1) / up_mt);
         if (M <= 64 || wgs < 160) {
             up_mt = 64;
