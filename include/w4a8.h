@@ -37,7 +37,7 @@
  *   - An int32 sum of INT8 products is exact whatever the codes for K up to
  *     W4A8_EXACT_MAX_K (127 * 128 * 131072 < 2^31).  The GEMMs also take
  *     longer rows, whose sums are exact while they lie within int32;
- *     w4a8_moe and w4a8_gemm_lora do not.
+ *     w4a8_moe, w4a8_gemm_lora and w4a8_ffn do not.
  *   - Alignment (W4A8_ERR_ALIGNMENT otherwise): the byte and element
  *     arrays -- W, X, Xq, wq, wq8, s_u8, a_u8, Y and any workspace -- start
  *     on a 16-byte boundary (the kernels move them in 16-byte pieces); the

@@ -76,7 +76,8 @@ __device__ __forceinline__ void stream_body(
     const int* __restrict__ offsets, const float* __restrict__ fsc,
     const float* __restrict__ tsc, const LoraArgs& lora, const FfnRows& ffn = {}) {
     static_assert(GLU == 0 || (LORA == 0 && WK == kWkLQQ && NTW % 2 == 0), "pairs of tiles");
-    static_assert(HROWS == 0 || (HROWS <= 2 && LORA == 0 && GLU == 0 && WK == kWkLQQ && RB == 1), "few float rows");
+    static_assert(HROWS == 0 || (HROWS <= 2 && LORA == 0 && GLU == 0 && WK == kWkLQQ && RB == 1),
+                  "one or two float rows");
     static_assert(LORA == 0 || (OUT == 0 && WK == kWkLQQ), "adapters: W4A8 to fp16");
     constexpr bool W8 = WK == kWkW8;
     constexpr bool F8 = WK == kWkF8 || WK == kWkF8G;
