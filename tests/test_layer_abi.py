@@ -27,7 +27,8 @@ def test_norm_refusals():
                 dict(ot=-1), dict(eps=0.0), dict(eps=-1.0), dict(eps=nan), dict(eps=inf),
                 dict(xs=inf), dict(xs=nan), dict(ys=nan), dict(ys=-inf)):
         assert norm(**bad) == UNSUP, bad
-    for bad in (dict(M=-1), dict(M=1 << 22), dict(K=0), dict(K=-16), dict(K=24), dict(rows=0), dict(rows=-1),
+    for bad in (dict(M=-1), dict(M=1 << 22), dict(K=0), dict(K=-16), dict(K=24), dict(rows=0),
+                dict(rows=-1),
                 dict(rows=3, ids=None), dict(rows=5, ids=None)):
         assert norm(**bad) == SHAPE, bad
     assert norm(M=0, X=None, Y=None, yw=None, yb=None, gate=None, ids=None, Xout=None, out=None,

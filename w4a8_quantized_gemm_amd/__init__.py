@@ -848,8 +848,8 @@ def ffn(Xq, sx, w13, w2, act: int = ACT_SILU, dtype=torch.float16, out=None, wor
         ot = _float_type(out, "out", _HALF_TYPES)
         _ready(out, out.dtype, (M, H), dev, "out")
         ws, ws_ptr, ws_bytes = _workspace(workspace, ffn_workspace_size, (M, H, F), dev)
-        status = lib.w4a8_ffn(Xq.data_ptr(), sx.data_ptr(), *p13, *p2, act, out.data_ptr(), ot, M, H,
-                              F, g, ws_ptr, ws_bytes, _raw_stream(dev.index))
+        status = lib.w4a8_ffn(Xq.data_ptr(), sx.data_ptr(), *p13, *p2, act, out.data_ptr(), ot, M,
+                              H, F, g, ws_ptr, ws_bytes, _raw_stream(dev.index))
     if status:
         _check(status, "w4a8_ffn")
     return out

@@ -892,8 +892,8 @@ W4A8_EXPORT w4a8_status_t w4a8_ffn(const int8_t* Xq, const float* sx, const uint
     if (e != hipSuccess) return hip_status(e);
     const int out = out_type == W4A8_IN_BF16 ? 2 : 0;
     if (p.down_rows)
-        return hip_status(w4a8::launch_w4a8_stream_rows(h, tops, lay.ntops, wq2, s2, a2, sw2, Y, out,
-                                                        M, H, F, group, p.down, stream));
+        return hip_status(w4a8::launch_w4a8_stream_rows(h, tops, lay.ntops, wq2, s2, a2, sw2, Y,
+                                                        out, M, H, F, group, p.down, stream));
     e = w4a8::launch_ffn_quant(h, tops, lay.ntops, M, F, hq, sh, stream);
     if (e != hipSuccess) return hip_status(e);
     if (p.down_stream)

@@ -412,7 +412,9 @@ __global__ __launch_bounds__(1024) void norm_long_kernel(NormArgs a) {
         if (!quantised)
             store_row8(a.out, a.out_type, m, K, i, v);
         else
-            q[i] = s != s ? uint2{0, 0} : a.out_type == 3 ? int8_codes(v, s, inv) : e4m3_codes(v, s);
+            q[i] = s != s ? uint2{0, 0}
+                   : a.out_type == 3 ? int8_codes(v, s, inv)
+                                     : e4m3_codes(v, s);
     }
 }
 
