@@ -40,6 +40,7 @@
 #include <type_traits>
 
 #include "ffn_common.h"
+#include "k_parts.h"
 #include "launch.h"
 #include "lora_common.h"
 #include "mfma_common.h"
@@ -528,22 +529,23 @@ __device__ __forceinline__ void mfma16_body(
     // K is cut into splits * KIN parts; this wave takes part ks * KIN + kp
     const int parts = splits * KIN;
     const int pidx = ks * KIN + kp;
-    const int kt0 = (int)((long long)KTall * pidx / parts);
-    const int KT = (int)((long long)KTall * (pidx + 1) / parts) - kt0;  // >= 1
+    const int kt0 = k_part_first(KTall, pidx, parts);
+    const int KT = k_part_first(KTall, pidx + 1, parts) - kt0;  // (0: k_parts.h)
     // Every wave of the workgroup runs the same number of K-steps (one
     // barrier per step): the longest part's, in pairs with a single loop
     // exit.  Steps past a wave's own part read an X tile of zeros (their
-    // weights are the part's last real step's, so no load leaves the part's
-    // K range).
+    // weights are the part's last real step's, so no load leaves the row's
+    // K-tiles).
     int KTmax = KT;
     if constexpr (KIN == 2) {
         const int q0 = ks * KIN;
-        const int a0 = (int)((long long)KTall * q0 / parts);
-        const int a1 = (int)((long long)KTall * (q0 + 1) / parts);
-        const int a2 = (int)((long long)KTall * (q0 + 2) / parts);
+        const int a0 = k_part_first(KTall, q0, parts);
+        const int a1 = k_part_first(KTall, q0 + 1, parts);
+        const int a2 = k_part_first(KTall, q0 + 2, parts);
         KTmax = max(a1 - a0, a2 - a1);
     }
     const int KTe = KTmax + (KTmax & 1);
+    const int KTlast = k_last_step<KIN>(KT);
     const int groups = K / GROUP;
 
     // ---- X straight into LDS (same tile format and load mapping as the
@@ -618,7 +620,7 @@ __device__ __forceinline__ void mfma16_body(
     Par16 pp;       // parameters of the raw set being decoded
     v4i B[4][2];
     v4i ring[4];
-    const int k1 = min(1, KTe - 1), kw1 = min(1, KT - 1);
+    const int k1 = min(1, KTe - 1), kw1 = min(1, KTlast);
     unsigned bc = 0, bn = XSTEP, bd = 2 * XSTEP;  // LDS tiles of X(kt), X(kt+1), X(kt+2)
 #pragma unroll
     for (int p = 0; p < CPT; ++p) x_load(0, p, bc);
@@ -670,7 +672,7 @@ __device__ __forceinline__ void mfma16_body(
     constexpr int XS = GS + kLoads;
     static_assert(XS + CPT <= SLOTS - 4, "X loads must precede the barrier");
     auto step = [&](int kt, unsigned cur, unsigned nxt, unsigned dst, Raw& wcur, Raw& wnx) {
-        const int k2 = min(kt + 2, KTe - 1), kw2 = min(kt + 2, KT - 1);
+        const int k2 = min(kt + 2, KTe - 1), kw2 = min(kt + 2, KTlast);
         Tmp16 tmp;
         static_for<SLOTS>([&](auto sc) {
             constexpr int s = decltype(sc)::value;
