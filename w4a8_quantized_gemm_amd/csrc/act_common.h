@@ -70,6 +70,23 @@ __device__ __forceinline__ unsigned quant4_fast(float a, float b, float c, float
     return w;
 }
 
+// OCP e4m3 codes of eight quotients of a row's elements and its scale: nearest even,
+// saturating at 448.  While the scale is a normal float32 they stay below
+// 448 (1 + 2^-23); a subnormal one is a whole number of 2^-149, and a quotient may
+// reach 671, of which the conversion alone makes the NaN code.
+__device__ __forceinline__ uint2 e4m3_codes8(const float (&t)[8]) {
+    float c[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) c[e] = __builtin_amdgcn_fmed3f(t[e], -448.0f, 448.0f);
+    unsigned w[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const int l = __builtin_amdgcn_cvt_pk_fp8_f32(c[4 * h], c[4 * h + 1], 0, false);
+        w[h] = (unsigned)__builtin_amdgcn_cvt_pk_fp8_f32(c[4 * h + 2], c[4 * h + 3], l, true);
+    }
+    return uint2{w[0], w[1]};
+}
+
 // Elements of float32, fp16 or bf16 rows (IN = 0, 1, 2).
 template <int IN>
 struct Row8 {  // eight consecutive elements of a row, widened to float32
@@ -173,23 +190,16 @@ __device__ __forceinline__ void quant_row_regs(const void* row, int K, uint8_t* 
             out[i] = uint2{b[0] | (b[1] << 8) | (b[2] << 16) | (b[3] << 24),
                            b[4] | (b[5] << 8) | (b[6] << 16) | (b[7] << 24)};
         } else {
-            // |x / s| <= 448 (1 + 2^-23) here, where the hardware conversion
-            // (nearest even) gives OCP e4m3's codes; a NaN quotient (NaN
-            // input) gets 0x7F whatever its sign
+            // a NaN quotient (NaN input) gets 0x7F whatever its sign
             float t[8];
 #pragma unroll
             for (int e = 0; e < 8; ++e) t[e] = __fdiv_rn(r.v[e], s);
-            unsigned w[2];
+            const uint2 codes = e4m3_codes8(t);
+            unsigned w[2] = {codes.x, codes.y};
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const int l = __builtin_amdgcn_cvt_pk_fp8_f32(t[4 * h], t[4 * h + 1], 0, false);
-                w[h] = (unsigned)__builtin_amdgcn_cvt_pk_fp8_f32(t[4 * h + 2], t[4 * h + 3], l,
-                                                                  true);
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    if (t[4 * h + e] != t[4 * h + e])
-                        w[h] = (w[h] & ~(0xFFu << (8 * e))) | (0x7Fu << (8 * e));
-            }
+            for (int e = 0; e < 8; ++e)
+                if (t[e] != t[e])
+                    w[e / 4] = (w[e / 4] & ~(0xFFu << (8 * (e % 4)))) | (0x7Fu << (8 * (e % 4)));
             out[i] = uint2{w[0], w[1]};
         }
     }

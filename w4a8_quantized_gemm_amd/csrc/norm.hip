@@ -150,13 +150,7 @@ __device__ __forceinline__ uint2 e4m3_codes(const float (&n)[8], float s) {
     float t[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) t[j] = __fdiv_rn(n[j], s);
-    unsigned w[2];
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        const int l = __builtin_amdgcn_cvt_pk_fp8_f32(t[4 * h], t[4 * h + 1], 0, false);
-        w[h] = (unsigned)__builtin_amdgcn_cvt_pk_fp8_f32(t[4 * h + 2], t[4 * h + 3], l, true);
-    }
-    return uint2{w[0], w[1]};
+    return e4m3_codes8(t);
 }
 
 }  // namespace
