@@ -14,7 +14,8 @@ if not torch.cuda.is_available():
 
 import w4a8_quantized_gemm_amd as w4  # noqa: E402
 from test_gpu_layer import same_bits  # noqa: E402
-from test_gpu_selection import DEV, say  # noqa: E402
+from selection_refs import decode_weights  # noqa: E402
+from test_gpu_selection import DEV, f64, host, say  # noqa: E402
 
 
 def subnormal_rows(K):
@@ -50,3 +51,65 @@ def test_subnormal_rows(K):
             same_bits(codes, q)
             if out == "e4m3":
                 assert np.abs(oracle.e4m3_decode(q)).max() == 448.0
+
+
+# -------------------------------------------------------------------- ffn ---
+
+def packed(W, g):
+    """Packed weights of W, their decoded INT8 values and channel scales."""
+    N, K = W.shape
+    p = w4.pack(torch.from_numpy(W).to(DEV), group=g)
+    W8 = decode_weights(host(p["wq"]).ravel(), host(p["s_u8"]).ravel(), host(p["a_u8"]).ravel(),
+                        N, K, g)
+    return p, W8, host(p["sw"])
+
+
+def selection(n, g):
+    """Packed [n][n] weights of one nonzero INT8 weight a row, on the diagonal, and
+    that weight: the product is then each channel's own code."""
+    p, W8, _ = packed(np.eye(n, dtype=np.float32), g)
+    w = int(W8[0, 0])
+    assert w > 0 and (W8 == w * np.eye(n, dtype=W8.dtype)).all()
+    return p, w
+
+
+@pytest.mark.parametrize("M", [1, 2, 15, 64, 300, 1300])
+def test_ffn_codes_of_small_activations(M):
+    """Codes of h where every gate lies between -40 and -75.
+
+    exp(-g) evaluated to one unit in the last place (2 u, u = 2^-24), the sum, the
+    quotient and the product (u each) put h within 5 u of its value, the row's
+    largest |h| likewise, and the scale and a code's quotient add u each: a code may
+    differ from that of the float64 quotient q only where q lies within 12 u |q|
+    of a half.  A power of the rounded product g log2(e) would be off by up to
+    |g| u = 75 u alone."""
+    n, g = 2048, 64
+    say(f"ffn small activations M={M}")
+    rng = np.random.default_rng(M)
+    w = rng.random((2 * n, n), dtype=np.float32)
+    w[:n] = -0.5 - 0.5 * w[:n]                     # gate: sums of one sign
+    w[n:] = w[n:] - 0.5                            # up: any
+    w13, W13, sw13 = packed(w, g)
+    w2, one = selection(n, g)
+    q = rng.integers(60, 128, (M, n)).astype(np.int8)
+    acc = (torch.from_numpy(q).double() @ torch.from_numpy(W13).double().t()).numpy()
+    scale = np.float32(55.0 / np.abs((acc[:, :n] * sw13[:n]).mean()))
+    s = (scale * rng.uniform(0.9, 1.1, M)).astype(np.float32)
+    gu = (acc.astype(np.float32) * s[:, None]) * sw13
+    assert gu.dtype == np.float32
+    a, b = gu[:, :n].astype(np.float64), gu[:, n:].astype(np.float64)
+    assert -75 < a.min() and a.max() < -40
+    h = a / (1.0 + np.exp(-a)) * b
+    sh = np.abs(h).max(1, keepdims=True) / 127.0
+    quot = h / sh
+    # (the down product's channel scale only brings the outputs near the codes)
+    by = 1.0 / (one * sh.mean())
+    w2["sw"] = torch.full((n,), by, dtype=torch.float32, device=DEV)
+    Y = w4.ffn(torch.from_numpy(q).to(DEV), torch.from_numpy(s).to(DEV), w13, w2)
+    got = f64(Y) / (one * sh * float(np.float32(by)))
+    code = np.rint(got)
+    assert bool(np.abs(got - code).max() < 0.07)   # fp16: 127 x 2^-11
+    near = np.abs(np.abs(quot - np.floor(quot)) - 0.5) <= 12 * 2.0 ** -24 * np.abs(quot)
+    assert bool(near.mean() < 1e-3)
+    bad = (code != np.rint(quot)) & ~near
+    assert not bad.any(), (int(bad.sum()), quot[bad][:5], code[bad][:5])
