@@ -1,5 +1,8 @@
 """Values, sizes and kernels at the borders of the norm with quantisation and of
 the gated feed-forward block, on the GPU (references: layer_refs.py)."""
+import math
+from fractions import Fraction
+
 import numpy as np
 import pytest
 
@@ -51,6 +54,63 @@ def test_subnormal_rows(K):
             same_bits(codes, q)
             if out == "e4m3":
                 assert np.abs(oracle.e4m3_decode(q)).max() == 448.0
+
+
+def squares(S, K):
+    """K integers below 2^24 whose squares add up to S < 2^53 (so every sum of
+    some of them is exact in float64, in any order)."""
+    x = [math.isqrt(S // 40)] * 40
+    S -= 40 * x[0] ** 2
+    while S:
+        x.append(math.isqrt(S))
+        S -= x[-1] ** 2
+    assert len(x) <= K and x[0] < 1 << 24
+    return np.array(x + [0] * (K - len(x)), np.float32)
+
+
+@pytest.mark.parametrize("K", [64, 80, 5008, 33024])
+def test_inverse_root_next_to_a_rounding_border(K):
+    """1 / sqrt(mean + eps) within some 2^-52 of the middle between two float32
+    numbers: the definition's float64 operations decide on which side it falls."""
+    rng = np.random.default_rng(K)
+    M = 3000 if K < 100 else 120
+    rows = []
+    for i in range(M):
+        m = (1 << 24) + int(rng.integers(1 << 24))             # 25 bits, odd: a middle
+        b = (2 * (m // 2) + 1) / float(1 << 24)                # in [1, 2)
+        b *= 2.0 ** math.floor(math.log2(math.sqrt(K / 2.0 ** 53)) + 1)
+        S = int(round(Fraction(K) / (Fraction(b) * Fraction(b)))) + i % 7 - 3
+        while S >= 1 << 53:
+            S >>= 2                                            # (the same middle, doubled)
+        rows.append(squares(S, K))
+    x = np.stack(rows)
+    w = np.ones(K, np.float32)
+    say(f"inverse root K={K}")
+    _, n = ref.norm(x, weight=w, eps=1e-30)
+    d = dict(weight=torch.from_numpy(w).to(DEV), eps=1e-30, out_type=w4.NORM_OUT_F32)
+    got = w4.norm_quant(torch.from_numpy(x).to(DEV), **d)
+    same_bits(got["out"], n)
+
+
+# (widths of which a product with the rounded 1 / K misses some of these quotients)
+@pytest.mark.parametrize("K", [784, 1968, 5152, 38576])
+def test_mean_next_to_a_rounding_border(K):
+    """Rows of two neighbouring float32 numbers, half each: the mean is exactly the
+    middle between them, and rounds to the even one."""
+    rng = np.random.default_rng(K)
+    M = 400 if K < 1000 else 40
+    lo = rng.uniform(1.0, 2.0, (M, 1)).astype(np.float32) * 2.0 ** rng.integers(-30, 30, (M, 1))
+    lo = lo.astype(np.float32)
+    hi = np.nextafter(lo, np.float32(np.inf))
+    x = np.where(rng.permuted(np.tile(np.arange(K) % 2, (M, 1)), axis=1) == 0, lo, hi)
+    x *= np.where(np.arange(M) % 2, 1, -1).astype(np.float32)[:, None]
+    w = np.ones(K, np.float32)
+    say(f"mean K={K}")
+    _, n = ref.norm(x, weight=w, layer=True, eps=1e-30)
+    d = dict(weight=torch.from_numpy(w).to(DEV), eps=1e-30, kind=w4.NORM_LAYER,
+             out_type=w4.NORM_OUT_F32)
+    got = w4.norm_quant(torch.from_numpy(x).to(DEV), **d)
+    same_bits(got["out"], n)
 
 
 # -------------------------------------------------------------------- ffn ---
