@@ -511,8 +511,8 @@ enum {
  *   W4A8_NORM_LAYER: u = float32(mean(v)), d = v - u,
  *                    r = float32(1 / sqrt(mean(d^2) + eps));  (d r) w + c
  *   c = NULL adds nothing.  Weights and biases are float32 [K].
- * The float64 sums make codes and scales the same on every path of the
- * library: a function of the inputs alone.
+ * The float64 sums are taken in an order that K alone fixes: a row's results
+ * are a function of its own inputs, whatever the rows beside it.
  *   X, Xout: [M][K] of x_type; Y: [M][K], gate: [gate_rows][K] of y_type
  *     (W4A8_IN_*; not read with Y NULL).
  *   g = gate_ids[m] with gate_ids (int32 [M]; a value outside [0, gate_rows)

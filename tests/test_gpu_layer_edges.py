@@ -113,6 +113,31 @@ def test_mean_next_to_a_rounding_border(K):
     same_bits(got["out"], n)
 
 
+@pytest.mark.parametrize("K", [512, 1024, 2048, 4096, 5120, 8192, 16384, 33024])
+@pytest.mark.parametrize("layer", [False, True])
+def test_rows_do_not_depend_on_their_batch(K, layer):
+    """The same rows alone, in a small and in a large batch: the same bits, also
+    where sums cancel (values of both signs far above the others), whose result
+    is a matter of the order of the additions."""
+    rng = np.random.default_rng(K)
+    M = 300
+    x = rng.standard_normal((M, K)).astype(np.float32)
+    for i in range(0, M, 2):
+        at = rng.permutation(K)[:K // 8]
+        big = np.exp2(rng.uniform(20, 90, len(at) // 2)).astype(np.float32)
+        x[i, at[:len(big)]], x[i, at[len(big):2 * len(big)]] = big, -big
+    w = np.ones(K, np.float32)
+    d = dict(weight=torch.from_numpy(w).to(DEV), out_type=w4.NORM_OUT_F32,
+             kind=w4.NORM_LAYER if layer else w4.NORM_RMS)
+    dx = torch.from_numpy(x).to(DEV)
+    say(f"rows alone and in a batch K={K} layer={layer}")
+    want = host(w4.norm_quant(dx, **d)["out"])
+    for m in (1, 7, 256):
+        for at in (0, M - m):
+            got = host(w4.norm_quant(dx[at:at + m].contiguous(), **d)["out"])
+            assert np.array_equal(got, want[at:at + m]), (m, at)
+
+
 # -------------------------------------------------------------------- ffn ---
 
 def packed(W, g):

@@ -7,10 +7,11 @@
 // norm(v) = (v r) w + bias with r = 1 / sqrt(mean(v^2) + eps) (RMS), or of
 // d = v - mean(v) (layer norm).  Every float32 operation is rounded by itself
 // (no fused multiply-add), and the sums behind mean() are taken in float64 of
-// exact float32 terms: 29 bits below the float32 they are rounded to, so the
-// order of a sum does not show and the codes are a function of the inputs,
-// whatever the launch shape.  A float64 addition costs this chip what a
-// float32 one does.
+// exact float32 terms, in an order that K alone fixes (launch_norm_types): a row's
+// codes are a function of its own inputs, whatever the batch.  Another order
+// would show where a signed sum cancels, and once in some 2^29 sums of squares,
+// which lie 29 bits below the float32 they are rounded to.  A float64 addition
+// costs this chip what a float32 one does.
 //
 // One workgroup per row, the row in registers between the reductions: X, Y
 // and the gate are read once and each output is written once.  Many rows are
@@ -430,15 +431,19 @@ __global__ __launch_bounds__(1024) void norm_long_kernel(NormArgs a) {
 
 namespace {
 
-// Threads and chunks of eight elements a thread for a row: two chunks a thread
-// where that is possible, fewer threads only where many rows share the CUs.  us,
-// threads x chunks (16-bit x and y to INT8, residual sum and norm):
-//   16 x 8192: 512 x 2 4.4, 1024 x 1 5.5, 256 x 4 5.4     8192 x 1024: 64 x 2 15.6,
-//   1 x 4096: 256 x 2 3.1, 1024 x 1 3.3, 64 x 8 6.4         256 x 1 20.1
-//   16 x 2048: 256 x 2 3.6, 128 x 2 3.9, 1024 x 1 3.8     8192 x 2048: 128 x 2 25.5,
-//   8192 x 8192: 512 x 2 84, 256 x 4 89, 1024 x 1 112       256 x 1 28.0, 64 x 4 28.2
-//   8192 x 4096: 256 x 2 44.4, 512 x 1 50.4               2048 x 16384: 512 x 4 51.1,
-//   1000 x 5120 (gated, two norms): 256 x 3 13.9, 512 x 2 14.9   1024 x 2 54.5
+// Threads and chunks of eight elements a thread for a row, by its width alone: they
+// fix the order of the float64 sums, so a row gets the same bits in every batch.
+// Two chunks a thread where that is possible.  us, threads x chunks (16-bit x and y
+// to INT8, residual sum and norm):
+//   8192 x 8192: 512 x 2 84, 256 x 4 89, 1024 x 1 112     16 x 8192: 512 x 2 4.4,
+//   8192 x 4096: 256 x 2 44.4, 512 x 1 50.4                 1024 x 1 5.5, 256 x 4 5.4
+//   2048 x 16384: 512 x 4 51.1, 1024 x 2 54.5             1 x 4096: 256 x 2 3.1,
+//   8192 x 2048: 128 x 2 25.5, 256 x 1 28.0, 64 x 4 28.2    1024 x 1 3.3, 64 x 8 6.4
+//   8192 x 1024: 64 x 2 15.6, 256 x 1 20.1
+// Few rows alone would take more threads there (16 x 2048: 256 x 2 3.6, 128 x 2 4.1;
+// 256 x 1024: 3.9 against 4.2), and 256 x 3 saves many rows of 4112 .. 6144 little
+// (1000 x 5120, two norms: 14.1 against 14.5) but costs few a lot (16 x 5120: 4.8
+// against 4.1).
 template <int XT, int YT>
 void launch_norm_types(const NormArgs& a, hipStream_t st) {
     const int n8 = a.K / 8;
@@ -449,12 +454,9 @@ void launch_norm_types(const NormArgs& a, hipStream_t st) {
                            dim3(rows * TPB), 0, st, a);                                  \
         return;                                                                          \
     }
-    if (a.M > 256) {
-        NORM(2, 64)
-        NORM(2, 128)
-    }
+    NORM(2, 64)
+    NORM(2, 128)
     NORM(2, 256)
-    if (a.M > 256) NORM(3, 256)
     NORM(2, 512)
     NORM(3, 512)
     NORM(4, 512)
