@@ -565,6 +565,24 @@ w4a8_status_t w4a8_ffn(const int8_t* Xq, const float* sx, const uint8_t* wq13,
                        int group, void* workspace, size_t workspace_bytes,
                        hipStream_t stream);
 
+/*
+ * The kernels w4a8_ffn takes for a block (computed on the host from M, H and F),
+ * as w4a8_gemm_plan reports a GEMM's.  product 0: gate and up, 1: down.  Outputs:
+ *   *kernel         0 = streamed-tile kernel, 1 = tile kernel on 16 x 16 x 64
+ *                   instructions, 2 = tile kernel on 32 x 32 x 32 instructions,
+ *                   3 = streamed-tile kernel that quantises its rows of h;
+ *   *tile_rows      rows per workgroup;
+ *   *tile_channels  channels per workgroup (gate and up: of h, which are so many
+ *                   of each half);
+ *   *splits, *k_parts  as w4a8_gemm_plan.
+ * M = 0 reports the streamed kernels.  W4A8_ERR_NULL_PTR if an output pointer is
+ * NULL; W4A8_ERR_SHAPE for sizes that w4a8_ffn rejects, W4A8_ERR_UNSUPPORTED for
+ * another product.
+ */
+w4a8_status_t w4a8_ffn_plan(int M, int H, int F, int product, int* kernel,
+                            int* tile_rows, int* tile_channels, int* splits,
+                            int* k_parts);
+
 /* Static English text for a status code (never NULL). */
 const char* w4a8_status_str(w4a8_status_t status);
 

@@ -16,9 +16,10 @@ if not torch.cuda.is_available():
     pytest.skip("needs a GPU", allow_module_level=True)
 
 import w4a8_quantized_gemm_amd as w4  # noqa: E402
-from test_gpu_layer import same_bits  # noqa: E402
+from ffn_cases import CASES  # noqa: E402
+from test_gpu_layer import block, rows, run_ffn, same_bits  # noqa: E402
 from selection_refs import decode_weights  # noqa: E402
-from test_gpu_selection import DEV, f64, host, say  # noqa: E402
+from test_gpu_selection import DEV, f64, host, say, within  # noqa: E402
 
 
 def subnormal_rows(K):
@@ -74,7 +75,7 @@ def test_inverse_root_next_to_a_rounding_border(K):
     numbers: the definition's float64 operations decide on which side it falls."""
     rng = np.random.default_rng(K)
     M = 3000 if K < 100 else 120
-    rows = []
+    x = []
     for i in range(M):
         m = (1 << 24) + int(rng.integers(1 << 24))             # 25 bits, odd: a middle
         b = (2 * (m // 2) + 1) / float(1 << 24)                # in [1, 2)
@@ -82,8 +83,8 @@ def test_inverse_root_next_to_a_rounding_border(K):
         S = int(round(Fraction(K) / (Fraction(b) * Fraction(b)))) + i % 7 - 3
         while S >= 1 << 53:
             S >>= 2                                            # (the same middle, doubled)
-        rows.append(squares(S, K))
-    x = np.stack(rows)
+        x.append(squares(S, K))
+    x = np.stack(x)
     w = np.ones(K, np.float32)
     say(f"inverse root K={K}")
     _, n = ref.norm(x, weight=w, eps=1e-30)
@@ -198,3 +199,14 @@ def test_ffn_codes_of_small_activations(M):
     assert bool(near.mean() < 1e-3)
     bad = (code != np.rint(quot)) & ~near
     assert not bad.any(), (int(bad.sum()), quot[bad][:5], code[bad][:5])
+
+
+@pytest.mark.parametrize("M,H,F,g,act,dt", CASES)
+def test_ffn_forms(M, H, F, g, act, dt):
+    """Every kernel that a plan can choose (ffn_cases.py)."""
+    say(f"ffn form M={M} H={H} F={F} g={g} {act} {dt} {w4.ffn_plan(M, H, F)}")
+    w13, w2, dec = block(H, F, g, 1)
+    q, s = rows(M, H, M + H)
+    Y = run_ffn(q, s, w13, w2, act, dt)
+    want, tol = ref.ffn(q, s, *dec, act, dt)
+    within(f64(Y), want, tol)

@@ -53,7 +53,7 @@ EXPORTS = ("w4a8_pack", "w4a8_quant_act", "w4fp8_quant_act",
            "w4fp8g_gemm", "w8a8_pack", "w8a8_gemm",
            "w4a8_route_workspace_size", "w4a8_route", "w4a8_moe_workspace_size", "w4a8_moe",
            "w4a8_gemm_lora_workspace_size", "w4a8_gemm_lora",
-           "w4a8_norm_quant", "w4a8_ffn_workspace_size", "w4a8_ffn",
+           "w4a8_norm_quant", "w4a8_ffn_workspace_size", "w4a8_ffn", "w4a8_ffn_plan",
            "w4a8_status_str", "w4a8_last_hip_error", "w4a8_layout_version")
 
 _P, _I, _Z = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t
@@ -92,6 +92,7 @@ lib.w4a8_ffn_workspace_size.argtypes = [_I, _I, _I]
 lib.w4a8_ffn_workspace_size.restype = _Z
 lib.w4a8_ffn.argtypes = [_P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _I, _P, _I, _I, _I, _I, _I, _P, _Z,
                          _P]
+lib.w4a8_ffn_plan.argtypes = [_I, _I, _I, _I, _P, _P, _P, _P, _P]
 lib.w4a8_status_str.argtypes = [_I]
 lib.w4a8_status_str.restype = ctypes.c_char_p
 lib.w4a8_last_hip_error.restype = _I
@@ -100,7 +101,7 @@ for _n in ("w4a8_pack", "w4a8_quant_act", "w4fp8_quant_act", "w4a8_quant_act_ex"
            "w4fp8_quant_act_ex", "w4a8_gemm", "w4a8_gemm_noalloc", "w4a8_gemm_ablation", "w4a8_gemm_grouped",
            "w4fp8_gemm", "w4fp8g_pack", "w4fp8g_gemm", "w8a8_pack", "w8a8_gemm",
            "w4a8_gemm_plan", "w4a8_route", "w4a8_moe", "w4a8_gemm_lora", "w4a8_norm_quant",
-           "w4a8_ffn"):
+           "w4a8_ffn", "w4a8_ffn_plan"):
     getattr(lib, _n).restype = _I
 
 assert lib.w4a8_layout_version() == LAYOUT_VERSION
@@ -818,6 +819,22 @@ def norm_quant(x, weight=None, bias=None, y=None, y_weight=None, y_bias=None, ga
 
 def ffn_workspace_size(M: int, H: int, F: int) -> int:
     return int(lib.w4a8_ffn_workspace_size(M, H, F))
+
+
+def ffn_plan(M: int, H: int, F: int) -> dict:
+    """The kernels w4a8_ffn takes for its gate and up products ("up") and its down
+    product ("down"), as gemm_plan reports them (host-side, no GPU).  Kernel
+    "rows": the streamed one that quantises its rows of h."""
+    plans = {}
+    for product, name in enumerate(("up", "down")):
+        vals = [ctypes.c_int(0) for _ in range(5)]
+        _check(lib.w4a8_ffn_plan(M, H, F, product, *[ctypes.addressof(v) for v in vals]),
+               "w4a8_ffn_plan")
+        kernel, rows, chans, splits, parts = (v.value for v in vals)
+        plans[name] = {"kernel": ("stream", "tile16", "tile32", "rows")[kernel],
+                       "tile_rows": rows, "tile_channels": chans, "splits": splits,
+                       "k_parts": parts}
+    return plans
 
 
 def ffn(Xq, sx, w13, w2, act: int = ACT_SILU, dtype=torch.float16, out=None, workspace=None,

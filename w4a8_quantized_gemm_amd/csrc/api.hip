@@ -855,6 +855,34 @@ W4A8_EXPORT size_t w4a8_ffn_workspace_size(int M, int H, int F) {
     return FfnLayout(M, H, F).bytes;
 }
 
+W4A8_EXPORT w4a8_status_t w4a8_ffn_plan(int M, int H, int F, int product, int* kernel,
+                                        int* tile_rows, int* tile_channels, int* splits,
+                                        int* k_parts) {
+    if (product != 0 && product != 1) return W4A8_ERR_UNSUPPORTED;
+    if (!kernel || !tile_rows || !tile_channels || !splits || !k_parts) return W4A8_ERR_NULL_PTR;
+    if (!valid_ffn(M, H, F)) return W4A8_ERR_SHAPE;
+    const FfnPlan p(M, H, F);
+    auto report = [&](int kind, int rows, int channels, int parts, int waves) {
+        *kernel = kind;
+        *tile_rows = rows;
+        *tile_channels = channels;
+        *splits = parts;
+        *k_parts = waves;
+    };
+    if (product == 0) {
+        if (p.up_stream) report(0, 16 * p.up.rb, 8 * p.up.nt_per_wave, 1, p.up.ks);
+        else report(1, p.up_mt, w4a8::kNT / 2 / p.up_kin, 1, p.up_kin);
+    } else if (p.down_stream) {
+        report(p.down_rows ? 3 : 0, 16 * p.down.rb, 16 * p.down.nt_per_wave, 1, p.down.ks);
+    } else if (p.down64) {
+        report(1, 64, w4a8::kNT / 2, p.down_splits, 2);
+    } else {
+        const w4a8::MfmaPlan& d = p.down_plan;
+        report(d.mt16 ? 1 : 2, d.mt16 ? d.mt16 : d.mt, w4a8::kNT / d.kin, d.splits, d.kin);
+    }
+    return W4A8_OK;
+}
+
 W4A8_EXPORT w4a8_status_t w4a8_ffn(const int8_t* Xq, const float* sx, const uint8_t* wq13,
                                    const uint8_t* s13, const uint8_t* a13, const float* sw13,
                                    const uint8_t* wq2, const uint8_t* s2, const uint8_t* a2,
