@@ -187,6 +187,11 @@ __global__ __launch_bounds__(TPB == 64 ? 256 : TPB) void norm_kernel(NormArgs a)
     const int tid = TPB == 64 ? threadIdx.x & 63 : threadIdx.x;
     if (TPB == 64 && (int)m >= a.M) return;
 
+    // The gate is requested with the other rows, except where x, y and gate of
+    // float32 would take 96 of the 128 registers that 1024 threads have each (nine
+    // more went to scratch): there behind the norm of y (257 x 32768, layer norms:
+    // 71 -> 62 us).
+    constexpr bool kLateGate = XT == 0 && YT == 0 && CH * TPB == 4096;
     Raw8<XT> xr[CH];
     Raw8<YL> yr[HASY ? CH : 1], gr[HASY ? CH : 1];
     const void* xrow = row_at<XT>(a.x, m, K);
@@ -204,15 +209,17 @@ __global__ __launch_bounds__(TPB == 64 ? 256 : TPB) void norm_kernel(NormArgs a)
             yr[j] = i < n8 ? load_raw8<YL>(yrow, i) : Raw8<YL>{};
         }
         g = gate_row(a, (int)m);
-        if (g >= 0) {
-            const void* grow = row_at<YL>(a.gate, (size_t)g, K);
-#pragma unroll
-            for (int j = 0; j < CH; ++j) {
-                const int i = tid + TPB * j;
-                gr[j] = i < n8 ? load_raw8<YL>(grow, i) : Raw8<YL>{};
-            }
-        }
     }
+    auto load_gate = [&] {
+        const void* grow = row_at<YL>(a.gate, (size_t)g, K);
+#pragma unroll
+        for (int j = 0; j < CH; ++j) {
+            const int i = tid + TPB * j;
+            gr[j] = i < n8 ? load_raw8<YL>(grow, i) : Raw8<YL>{};
+        }
+    };
+    if constexpr (HASY && !kLateGate)
+        if (g >= 0) load_gate();
 
     // v = norm(v); elements past the row end stay zero
     auto normed = [&](float (&v)[CH][8], const float* w, const float* bias, int at) {
@@ -265,6 +272,7 @@ __global__ __launch_bounds__(TPB == 64 ? 256 : TPB) void norm_kernel(NormArgs a)
         }
         if (a.y_weight) normed(v, a.y_weight, a.y_bias, 0);
         if (g >= 0) {
+            if constexpr (kLateGate) load_gate();
 #pragma unroll
             for (int j = 0; j < CH; ++j) {
                 const Row8<YL> gv = widen8<YL>(gr[j]);
