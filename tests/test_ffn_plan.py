@@ -4,6 +4,7 @@ tests, so that a change of the rules cannot leave a kernel without a test."""
 import ast
 import ctypes
 import os
+import re
 
 import pytest
 
@@ -75,3 +76,22 @@ def test_plan_errors():
     assert plan(-1, 256, 384, 0, *ptrs) == 2 and plan(4, 200, 384, 0, *ptrs) == 2
     assert plan(4, 256, 64, 1, *ptrs) == 2 and plan(1 << 23, 256, 384, 1, *ptrs) == 2
     assert plan(4, 256, 384, 2, *ptrs) == 5 and plan(4, 256, 384, -1, *ptrs) == 5
+
+
+def test_no_streamed_kernel_without_a_plan():
+    """Compiled forms (tiles, row blocks) against those that plans choose: gate and
+    up with two or four tiles and one or two row blocks, bfloat16 results (of the
+    down product alone) with one, two or four tiles and one or two."""
+    from test_isa_hazards import HIPCC, OUT, _asm
+    if not os.path.exists(HIPCC):
+        pytest.skip("hipcc not available")
+    os.makedirs(OUT, exist_ok=True)
+
+    def compiled(src, pattern):
+        return {tuple(map(int, m)) for m in re.findall(pattern, _asm(src))}
+    glu = compiled("gemm_stream_glu.hip",
+                   r"w4a8_stream_glu_kernelILi(\d)ELi\dELi\d+ELb\dELi(\d)ELi\dEE")
+    assert glu == {(4, 1), (4, 2), (2, 1), (2, 2)}
+    bf16 = compiled("gemm_stream.hip",  # <tiles, stages, 2, group, parameters in LDS, W4A8, blocks>
+                    r"w4a8_stream_kernelILi(\d)ELi\dELi2ELi\d+ELb\dELi0ELi(\d)EE")
+    assert bf16 == {(4, 1), (4, 2), (2, 1), (2, 2), (1, 1), (1, 2)}

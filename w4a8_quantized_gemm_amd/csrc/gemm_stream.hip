@@ -51,23 +51,23 @@ static hipError_t w4a8_stream_ntw(const int8_t* X, const float* sx, const uint8_
 #define W4A8_LS(O, G, P)                                                                    \
     hipLaunchKernelGGL((w4a8_stream_kernel<NTW, D, O, G, P, kWkLQQ, RB>), grid, block, lds, \
                        st, X, sx, wq, s_u8, a_u8, sw, Y, M, N, K, ks, offsets)
-    if (ldsp) {
-        if (out_type == 1) {
-            if (group == 64) W4A8_LS(1, 64, true); else W4A8_LS(1, 128, true);
-        } else if (out_type == 2) {
-            if (group == 64) W4A8_LS(2, 64, true); else W4A8_LS(2, 128, true);
+#define W4A8_LS_GROUP(O, P)                                             \
+    do {                                                                \
+        if (group == 64) W4A8_LS(O, 64, P); else W4A8_LS(O, 128, P);    \
+    } while (0)
+    if (out_type == 2) {
+        // (the feed-forward block's down product, which takes no wider forms)
+        if constexpr (NTW <= 4 && RB <= 2) {
+            if (ldsp) W4A8_LS_GROUP(2, true); else W4A8_LS_GROUP(2, false);
         } else {
-            if (group == 64) W4A8_LS(0, 64, true); else W4A8_LS(0, 128, true);
+            return hipErrorInvalidValue;
         }
+    } else if (ldsp) {
+        if (out_type == 1) W4A8_LS_GROUP(1, true); else W4A8_LS_GROUP(0, true);
     } else {
-        if (out_type == 1) {
-            if (group == 64) W4A8_LS(1, 64, false); else W4A8_LS(1, 128, false);
-        } else if (out_type == 2) {
-            if (group == 64) W4A8_LS(2, 64, false); else W4A8_LS(2, 128, false);
-        } else {
-            if (group == 64) W4A8_LS(0, 64, false); else W4A8_LS(0, 128, false);
-        }
+        if (out_type == 1) W4A8_LS_GROUP(1, false); else W4A8_LS_GROUP(0, false);
     }
+#undef W4A8_LS_GROUP
 #undef W4A8_LS
     return hipGetLastError();
 }

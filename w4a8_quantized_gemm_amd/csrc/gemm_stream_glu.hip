@@ -126,7 +126,6 @@ hipError_t launch_w4a8_stream_glu(const int8_t* X, const float* sx, const uint8_
         case 4 * 8 + 2: GLU_NTW(4, 2, 2);
         case 2 * 8 + 1: GLU_NTW(2, 2, 1);
         case 2 * 8 + 2: GLU_NTW(2, 2, 2);
-        case 2 * 8 + 4: GLU_NTW(2, 2, 4);
         default: return hipErrorInvalidValue;
     }
 #undef GLU_NTW
