@@ -139,6 +139,21 @@ def test_rows_do_not_depend_on_their_batch(K, layer):
             assert np.array_equal(got, want[at:at + m]), (m, at)
 
 
+def test_empty_batch_with_its_gates():
+    """No rows, and so no gate of a row: nothing to do, as in the C entry."""
+    x = torch.zeros((0, 64), dtype=torch.bfloat16, device=DEV)
+    w = torch.ones(64, device=DEV)
+    ids = torch.zeros(0, dtype=torch.int32, device=DEV)
+    for gate in (x, torch.zeros((1, 64), dtype=torch.bfloat16, device=DEV)):
+        for more in ({}, dict(gate_ids=ids)):
+            r = w4.norm_quant(x, w, y=x, gate=gate, **more)
+            assert r["out"].shape == (0, 64) and r["sx"].shape == (0,)
+    one = torch.zeros((1, 64), dtype=torch.bfloat16, device=DEV)
+    for more in ({}, dict(gate_ids=torch.zeros(1, dtype=torch.int32, device=DEV))):
+        with pytest.raises(ValueError, match="rows"):
+            w4.norm_quant(one, w, y=one, gate=x, **more)
+
+
 # -------------------------------------------------------------------- ffn ---
 
 def packed(W, g):

@@ -765,7 +765,7 @@ def norm_quant(x, weight=None, bias=None, y=None, y_weight=None, y_bias=None, ga
             if not isinstance(gate, torch.Tensor) or gate.dim() != 2:
                 raise ValueError("gate must be a 2-D tensor [rows][K]")
             rows = gate.shape[0]
-            if rows < 1 or (gate_ids is None and rows not in (1, M)):
+            if (rows < 1 and M) or (gate_ids is None and rows not in (1, M)):
                 raise ValueError(f"gate must have 1 or {M} rows, or gate_ids; got {rows}")
             _ready(gate, y.dtype, (rows, K), dev, "gate")
             gate_ptr = gate.data_ptr()
