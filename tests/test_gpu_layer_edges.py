@@ -154,6 +154,29 @@ def test_empty_batch_with_its_gates():
             w4.norm_quant(one, w, y=one, gate=x, **more)
 
 
+def test_result_names_every_output():
+    """out, sx and x are there whatever the caller's dict holds: x itself without
+    y, no scales for floating types; the dict is not changed."""
+    x = torch.randn((4, 64), device=DEV).to(torch.bfloat16)
+    w = torch.ones(64, device=DEV)
+    plain = w4.norm_quant(x, w)
+    old = torch.empty_like(x)
+    for into in ({"out": torch.empty((4, 64), dtype=torch.int8, device=DEV),
+                  "sx": torch.empty(4, device=DEV)},
+                 {"out": torch.empty((4, 64), dtype=torch.int8, device=DEV),
+                  "sx": torch.empty(4, device=DEV), "x": old}):
+        keys = dict(into)
+        r = w4.norm_quant(x, w, out=into)
+        assert r["x"] is x and r["out"] is into["out"] and r["sx"] is into["sx"]
+        assert torch.equal(r["out"], plain["out"]) and torch.equal(r["sx"], plain["sx"])
+        assert into == keys
+    for into in ({"out": old}, {"out": old, "sx": torch.empty(4, device=DEV), "x": x}):
+        r = w4.norm_quant(x, w, out_type=w4.NORM_OUT_BF16, out=into)
+        assert r["x"] is x and r["sx"] is None and r["out"] is old
+    full = {"out": old, "sx": None, "x": x}
+    assert w4.norm_quant(x, w, out_type=w4.NORM_OUT_BF16, out=full) is full
+
+
 # -------------------------------------------------------------------- ffn ---
 
 def packed(W, g):

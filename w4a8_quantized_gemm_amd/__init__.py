@@ -744,7 +744,8 @@ def norm_quant(x, weight=None, bias=None, y=None, y_weight=None, y_bias=None, ga
     Returns a dict with out ([M][K]: int8 or e4m3 bytes for the GEMMs, or a
     floating type for moe and gemm_lora), sx (float32 [M] scales; None for
     floating types) and x (the new residual stream in x's type; x itself
-    without y).  `out`: such a dict to write into; its x may be the input x."""
+    without y).  `out`: such a dict to write into, and what is returned if it names
+    all three so; its x may be the input x."""
     xt = _float_type(x, "x")
     _on_gpu(x, "x")
     M, K = shape = x.shape
@@ -814,6 +815,12 @@ def norm_quant(x, weight=None, bias=None, y=None, y_weight=None, y_bias=None, ga
                                      _raw_stream(dev.index))
     if status:
         _check(status, "w4a8_norm_quant")
+    if (y is None and out.get("x") is not x) or (not quantised and out.get("sx", out) is not None):
+        out = dict(out)  # (the caller's may hold buffers of other calls)
+        if y is None:
+            out["x"] = x
+        if not quantised:
+            out["sx"] = None
     return out
 
 
