@@ -248,3 +248,19 @@ def test_ffn_forms(M, H, F, g, act, dt):
     Y = run_ffn(q, s, w13, w2, act, dt)
     want, tol = ref.ffn(q, s, *dec, act, dt)
     within(f64(Y), want, tol)
+
+
+def test_ffn_refuses_packed_arrays_that_are_not_1d():
+    """As gemm_lora and moe do."""
+    rng = np.random.default_rng(1)
+    w13 = packed(rng.random((768, 256), dtype=np.float32), 64)[0]
+    w2 = packed(rng.random((256, 384), dtype=np.float32), 64)[0]
+    q = torch.zeros((4, 256), dtype=torch.int8, device=DEV)
+    s = torch.ones(4, device=DEV)
+    assert w4.ffn(q, s, w13, w2).shape == (4, 256)
+    for name in ("wq", "s_u8", "a_u8", "sw"):
+        for which, p in (("w13", w13), ("w2", w2)):
+            a = dict(w13=w13, w2=w2)
+            a[which] = dict(p, **{name: p[name].view(2, -1)})
+            with pytest.raises(ValueError, match=which):
+                w4.ffn(q, s, **a)

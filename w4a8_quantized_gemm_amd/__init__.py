@@ -575,23 +575,25 @@ def _packed_ready(p, keys, E, device, name):
 
 
 def _packed_ptrs(p, device, name):
-    """Addresses of one matrix's packed arrays, checked as _ready does."""
+    """Addresses of one matrix's packed arrays, checked as _packed_ready does."""
     wq, s, a, sw = p["wq"], p["s_u8"], p["a_u8"], p["sw"]
     N, i = p["N"], device.index
     n = N * p["K"]
-    try:
-        if (wq.numel() * 2 == n and wq.dtype is torch.uint8 and wq.get_device() == i
-                and wq.is_contiguous() and sw.numel() == N and sw.dtype is torch.float32
-                and sw.get_device() == i and sw.is_contiguous()):
-            n //= p["group"]
-            if (s.numel() == n and s.dtype is torch.uint8 and s.get_device() == i
-                    and s.is_contiguous() and a.numel() == n and a.dtype is torch.uint8
-                    and a.get_device() == i and a.is_contiguous()):
-                return wq.data_ptr(), s.data_ptr(), a.data_ptr(), sw.data_ptr()
+    g = n // p["group"]
+    try:  # (spelled out: small calls are bound by this)
+        ready = (wq.numel() == n // 2 and wq.dim() == 1 and wq.dtype is torch.uint8
+                 and wq.get_device() == i and wq.is_contiguous()
+                 and s.numel() == g and s.dim() == 1 and s.dtype is torch.uint8
+                 and s.get_device() == i and s.is_contiguous()
+                 and a.numel() == g and a.dim() == 1 and a.dtype is torch.uint8
+                 and a.get_device() == i and a.is_contiguous()
+                 and sw.numel() == N and sw.dim() == 1 and sw.dtype is torch.float32
+                 and sw.get_device() == i and sw.is_contiguous())
     except AttributeError:
-        pass
-    _packed_ready(p, ("wq", "s_u8", "a_u8", "sw"), 1, device, name)
-    raise ValueError(f"the packed arrays of {name} must be 1-D")
+        ready = False
+    if not ready:  # says which and why
+        _packed_ready(p, ("wq", "s_u8", "a_u8", "sw"), 1, device, name)
+    return wq.data_ptr(), s.data_ptr(), a.data_ptr(), sw.data_ptr()
 
 
 def route_workspace_size(T: int, E: int, k: int) -> int:
