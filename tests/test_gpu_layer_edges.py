@@ -19,7 +19,7 @@ import w4a8_quantized_gemm_amd as w4  # noqa: E402
 from ffn_cases import CASES  # noqa: E402
 from test_gpu_layer import block, rows, run_ffn, same_bits  # noqa: E402
 from selection_refs import decode_weights  # noqa: E402
-from test_gpu_selection import DEV, f64, host, say, within  # noqa: E402
+from test_gpu_selection import DEV, TYPES, f64, host, say, within  # noqa: E402
 
 
 def subnormal_rows(K):
@@ -264,3 +264,31 @@ def test_ffn_refuses_packed_arrays_that_are_not_1d():
             a[which] = dict(p, **{name: p[name].view(2, -1)})
             with pytest.raises(ValueError, match=which):
                 w4.ffn(q, s, **a)
+
+
+@pytest.mark.parametrize("H,F,g,dt", [(128, 1024, 64, "bf16"), (8192, 128, 128, "f16"),
+                                      (128, 128, 128, "f16")])
+def test_ffn_at_the_limit_of_its_rows(H, F, g, dt):
+    """M H or M F just below 2^31: h of 8 GiB, rows and results of up to 4.  The
+    batch repeats its first rows with an odd period, so every row is checked: the
+    first ones and the last against the reference, all against the first."""
+    M, P = ((1 << 31) - 1) // max(H, F), 4099
+    say(f"ffn limit M={M} H={H} F={F} {w4.ffn_plan(M, H, F)}")
+    assert w4.ffn_workspace_size(M + 1, H, F) == 0
+    w13, w2, dec = block(H, F, g, 7)
+    q, s = rows(P, H, 3)
+    at = torch.arange(M, device=DEV) % P
+    Xq = torch.from_numpy(q).to(DEV)[at]
+    sx = torch.from_numpy(s).to(DEV)[at]
+    Y = w4.ffn(Xq, sx, w13, w2, dtype=TYPES[dt])
+    want, tol = ref.ffn(q, s, *dec, "silu", dt)
+    within(f64(Y[:P]), want, tol)
+    last = at[M - 300:].cpu().numpy()
+    within(f64(Y[M - 300:]), want[last], tol[last])
+    bits = Y.view(torch.int16)
+    whole = M // P
+    for i in range(0, whole, 64):
+        n = min(64, whole - i)
+        part = bits[i * P:(i + n) * P].view(n, P, H)
+        assert bool((part == bits[:P]).all()), i
+    assert torch.equal(bits[whole * P:], bits[:M - whole * P])
