@@ -31,6 +31,8 @@ PLANS = {  # (M, H, F): gate and up, down
     (64, 8192, 28672): (("tile16", 64, 64, 1, 2), ("tile16", 64, 128, 8, 2)),
     (133, 2048, 1408): (("stream", 32, 16, 1, 4), ("stream", 32, 32, 1, 4)),
     (2048, 4096, 11008): (("tile16", 128, 128, 1, 1), ("tile32", 128, 256, 1, 1)),
+    (4096, 5120, 13824): (("tile16", 128, 128, 1, 1), ("tile16", 256, 256, 1, 1)),
+    (8192, 7168, 18944): (("tile16", 128, 128, 1, 1), ("tile16", 256, 256, 1, 1)),
     (4096, 8192, 28672): (("tile16", 256, 128, 1, 1), ("tile16", 256, 256, 1, 1)),
 }
 

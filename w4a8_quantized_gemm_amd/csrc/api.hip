@@ -770,9 +770,10 @@ struct FfnPlan {
         const w4a8::MfmaPlan p = w4a8::plan_w4a8_mfma(M, 2 * F, H);
         up_mt = p.mt16 ? p.mt16 : p.mt;
         // Short K: two 128-row workgroups per CU, one's epilogue beside the other's
-        // loop (8192 rows of A, whole block: 1046 against 1079; 4096 rows of B the
-        // other way, 2257 against 2216).
-        if (k_tiles(H) <= 32) up_mt = 128;
+        // loop (128 / 256 rows a tile, gate and up: 4096 x 5120 x 13824 524 / 550,
+        // 2048 x 6144 x 16384 357 / 367, 8192 x 7168 x 18944 1850 / 1958; B the other
+        // way, whole block: 4096 rows 2314 / 2282, 8192 rows 4683 / 4562).
+        if (k_tiles(H) <= 56) up_mt = 128;
         const long long wgs = (long long)(F / 128) * ((M + up_mt - 1) / up_mt);
         if (M <= 64 || wgs < 160) {
             up_mt = 64;
