@@ -345,7 +345,7 @@ FFN = [
     (1, 4096, 1408, 128, "gelu", "bf16"),
     (1, 256, 11008, 64, "silu", "f16"),
     (2, 384, 640, 128, "silu", "bf16"),
-    # up to four rows are quantised by the down product's workgroups
+    # from three rows on h is quantised by a kernel of its own
     (3, 1152, 384, 64, "silu", "f16"),
     (4, 4096, 1408, 128, "gelu", "bf16"),
     (4, 8192, 5504, 64, "silu", "bf16"),
@@ -363,7 +363,7 @@ FFN = [
     (33, 512, 11008, 64, "silu", "f16"),
     (47, 4096, 2688, 128, "gelu", "f16"),
     (63, 384, 8192, 128, "silu", "bf16"),
-    (64, 512, 384, 128, "silu", "f16"),      # tiles of 128 rows
+    (64, 512, 384, 128, "silu", "f16"),      # streamed, two row blocks
     (65, 384, 640, 64, "gelu", "bf16"),      # H not a multiple of 256
     (100, 2048, 1408, 64, "gelu", "f16"),
     (128, 1024, 4096, 128, "silu", "bf16"),
@@ -374,8 +374,8 @@ FFN = [
     (513, 4096, 384, 128, "gelu", "bf16"),
     (1000, 512, 5504, 64, "silu", "f16"),
     (2050, 256, 4224, 128, "silu", "bf16"),
-    # one case for each kernel that the plans choose: 64-row tiles of 64 channels
-    # of each half, of 128; 256-row tiles
+    # (test_ffn_plan.py compares the plans' forms with these sizes and ffn_cases.py)
+    # 64-row tiles of 128 channels of each half; 128-row tiles of many rows
     (300, 256, 11008, 64, "gelu", "f16"),
     (4296, 128, 8320, 128, "silu", "f16"),
     # down: 64-row tiles with their K split, and where 256 does not divide H

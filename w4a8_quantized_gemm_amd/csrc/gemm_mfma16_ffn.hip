@@ -3,11 +3,12 @@
 // tiles for the few rows between the streamed kernel's and the GEMM's own.
 //
 // A wave holds the gate and the up sums of the same 32 channels, so act(gate) up
-// is formed in registers: 4096 x 57344 x 8192 takes 1460 us (2.64 POP/s, matrix
-// cores busy 60 %) against 1486 with int32 sums written instead, which a second
-// kernel then needed 320 us to join.  64-row tiles are bound by the pace of one
-// workgroup's K-steps (64 x 57344 x 8192: 56 us for 242 MB of weights): loads
-// four steps ahead instead of two, or eight waves on four K parts, gained 5 %.
+// is formed in registers: 4096 x 57344 x 8192 takes 1454 us (2.65 POP/s, matrix
+// cores busy 57 %), 50 of them for the exponential and the quotient of the
+// activation; int32 sums written instead took 1486, and a second kernel 320 to
+// join them.  64-row tiles are bound by the pace of one workgroup's K-steps (64 x
+// 57344 x 8192: 57 us for 242 MB of weights): loads four steps ahead instead of
+// two, or eight waves on four K parts, gained 5 %.
 #include "mfma16_body.h"
 
 namespace w4a8 {

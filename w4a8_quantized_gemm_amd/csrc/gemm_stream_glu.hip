@@ -3,7 +3,7 @@
 // product of a few rows that its workgroups quantise themselves.
 //
 // Bound by the weights' stream: gate and up of 16 rows, 57344 x 8192, 42 us (5.75
-// TB/s), of one row of 22016 x 4096 12 us (4 TB/s: start, end and a wave's four
+// TB/s), of one row of 22016 x 4096 12.5 us (3.9 TB/s: start, end and a wave's four
 // K-tiles between them).  Quantising one row inside the down product costs it
 // nothing (11008 x 4096: 8.4 us either way) and saves a launch of 3-4 us; with
 // four rows it took 12.7 us against 9.8 and the launch.

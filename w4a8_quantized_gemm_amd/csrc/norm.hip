@@ -15,10 +15,12 @@
 //
 // One workgroup per row, the row in registers between the reductions: X, Y
 // and the gate are read once and each output is written once.  Many rows are
-// bound by memory (8192 x 8192, 16-bit X and Y to INT8: 470 MB in 84 us, 5.6
-// TB/s; the float64 sums cost nothing measurable there: 88 us with float32
-// ones against 89), fewer than a few per CU by one chain of loads, two or three
-// reductions and stores (2048 x 4096 gated: 75 MB in 20 us; 16 x 8192: 4.8 us).
+// bound by memory (8192 x 8192, 16-bit X and Y to INT8: 470 MB in 84-88 us, 5.3
+// to 5.6 TB/s; float32 X and Y: 872 MB in 156 us; the float64 sums cost nothing
+// measurable there: 88 us with float32 ones against 89).  A layer norm's second
+// reduction makes that 100 us, e4m3's rounded quotients 94.  Fewer rows than a few
+// per CU are bound by one chain of loads, two or three reductions and stores (2048
+// x 4096 gated: 75 MB in 21 us; 16 x 8192: 5 us).
 #include "act_common.h"
 #include "launch.h"
 #include "wave_common.h"
