@@ -17,7 +17,8 @@ if not torch.cuda.is_available():
 
 import w4a8_quantized_gemm_amd as w4  # noqa: E402
 from ffn_cases import CASES  # noqa: E402
-from test_gpu_layer import block, rows, run_ffn, same_bits  # noqa: E402
+from test_gpu_layer import (as_type, block, check_norm, norm_case, rows, run_ffn,  # noqa: E402
+                            same_bits)
 from selection_refs import decode_weights  # noqa: E402
 from test_gpu_selection import DEV, TYPES, f64, host, say, within  # noqa: E402
 
@@ -177,6 +178,37 @@ def test_result_names_every_output():
     assert w4.norm_quant(x, w, out_type=w4.NORM_OUT_BF16, out=full) is full
 
 
+def test_one_gate_by_ids():
+    """A single gate row that some rows name and others do not."""
+    M, K = 9, 272
+    d, r = norm_case(M, K, "bf16", "f16", True, "all", True)
+    ids = np.array([0, 1, -1, 0, 2, 0, -(1 << 31), (1 << 31) - 1, 0], np.int32)
+    d["gate_ids"], r["ids"] = torch.from_numpy(ids).to(DEV), ids
+    check_norm(d, r, "int8", False)
+    check_norm(d, r, "f32", True)
+
+
+@pytest.mark.parametrize("K", [16, 2064])
+def test_norm_of_the_most_rows(K):
+    """2^22 - 1 rows with an odd period: all against the first ones, and those
+    against the definition."""
+    M, P = (1 << 22) - 1, 1021
+    d, r = norm_case(P, K, "bf16", "f16", False, "none", True)
+    at = torch.arange(M, device=DEV) % P
+    out = w4.norm_quant(**dict(d, x=d["x"][at], y=d["y"][at]))
+    v, n = ref.norm(**r)
+    q, s = ref.codes(n, "int8")
+    same_bits(out["x"][:P], as_type(v, "bf16"))
+    same_bits(out["out"][:P], q)
+    same_bits(out["sx"][:P], s)
+    for t in (out["x"].view(torch.int16), out["out"], out["sx"].view(M, 1)):
+        whole = M // P
+        for i in range(0, whole, 256):
+            k = min(256, whole - i)
+            assert bool((t[i * P:(i + k) * P].view(k, P, -1) == t[:P]).all()), i
+        assert torch.equal(t[whole * P:], t[:M - whole * P])
+
+
 # -------------------------------------------------------------------- ffn ---
 
 def packed(W, g):
@@ -292,3 +324,62 @@ def test_ffn_at_the_limit_of_its_rows(H, F, g, dt):
         part = bits[i * P:(i + n) * P].view(n, P, H)
         assert bool((part == bits[:P]).all()), i
     assert torch.equal(bits[whole * P:], bits[:M - whole * P])
+
+
+@pytest.mark.parametrize("H,F", [(512, 640), (5120, 384)])
+def test_ffn_two_rows_do_not_touch_each_other(H, F):
+    """The down product quantises both rows in one workgroup: one that is not
+    finite is NaN, the other's results are those of the row alone."""
+    w13, w2, _ = block(H, F, 64, 8)
+    q, s = rows(2, H, 5)
+
+    def run(q, s):
+        return w4.ffn(torch.from_numpy(q).to(DEV), torch.from_numpy(s).to(DEV), w13, w2,
+                      dtype=torch.bfloat16)
+    alone = [run(q[i:i + 1], s[i:i + 1])[0] for i in range(2)]
+    both = run(q, s)
+    assert torch.equal(both[0], alone[0]) and torch.equal(both[1], alone[1])
+    for bad in (np.nan, np.inf, -np.inf, 3e38):
+        for i in range(2):
+            t = s.copy()
+            t[i] = bad
+            Y = run(q, t)
+            assert bool(torch.isnan(Y[i]).all()), (bad, i)
+            assert torch.equal(Y[1 - i], alone[1 - i]), (bad, i)
+    z = q.copy()
+    z[0] = 0
+    Y = run(z, s)
+    assert bool((Y[0] == 0).all()) and torch.equal(Y[1], alone[1])
+
+
+@pytest.mark.parametrize("act", ["silu", "gelu"])
+@pytest.mark.parametrize("M", [1, 2, 40, 300])
+def test_ffn_of_large_gates(act, M):
+    """Gates from 1e3 to 1e13 of either sign (GELU's cube leaves float32): act(g) u
+    is g u or 0, and codes and scale follow."""
+    n, g = 512, 128
+    rng = np.random.default_rng(M)
+    w = rng.standard_normal((2 * n, n)).astype(np.float32)
+    w[:n] = (0.5 + 0.5 * rng.random((n, n), dtype=np.float32)) * np.where(
+        rng.random((n, 1)) < 0.5, -1, 1).astype(np.float32)
+    w13, W13, sw13 = packed(w, g)
+    w2, one = selection(n, g)
+    q = rng.integers(60, 128, (M, n)).astype(np.int8)
+    acc = (torch.from_numpy(q).double() @ torch.from_numpy(W13).double().t()).numpy()
+    s = (10.0 ** rng.uniform(2, 12, M) / np.abs(acc[:, :n] * sw13[:n]).mean(1) * 10).astype(
+        np.float32)
+    gu = (acc.astype(np.float32) * s[:, None]) * sw13
+    a, b = gu[:, :n].astype(np.float64), gu[:, n:].astype(np.float64)
+    assert np.abs(a).min() > 700
+    h = np.where(a > 0, a * b, 0.0)
+    sh = np.abs(h).max(1, keepdims=True) / 127.0
+    by = (1.0 / (one * sh)).astype(np.float32)
+    for m in range(M):  # a channel scale for each row: results near the codes
+        if m and m % 40:
+            continue
+        w2["sw"] = torch.full((n,), float(by[m, 0]), dtype=torch.float32, device=DEV)
+        Y = w4.ffn(torch.from_numpy(q).to(DEV), torch.from_numpy(s).to(DEV), w13, w2,
+                   act=w4.ACT_GELU if act == "gelu" else w4.ACT_SILU)
+        got = f64(Y[m]) / (one * sh[m] * float(by[m, 0]))
+        # half a code, and the fp16 rounding of one
+        assert bool((np.abs(got - h[m] / sh[m]) <= 0.5 + 0.07).all())
